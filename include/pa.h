@@ -64,7 +64,8 @@ typedef enum {
   PA_ERR_WORKSPACE = -4,   /* workspace smaller than pa_workspace_bytes() */
   PA_ERR_RANGE = -5,       /* device: block ID, slot or context outside its table or pool */
   PA_ERR_CUDA = -6,        /* a CUDA runtime or driver call failed */
-  PA_ERR_TIMEOUT = -7      /* device: a bounded wait gave up */
+  PA_ERR_TIMEOUT = -7,     /* device: a bounded wait gave up */
+  PA_ERR_NO_BLOCKS = -8    /* device: the pool has too few free blocks for a sequence */
 } pa_status;
 
 /* Bit that a kernel ORs into *dev_status for device-detected error `code`. */
@@ -395,6 +396,222 @@ PA_API size_t pa_calibrate_bytes(void);
 PA_API int pa_calibrate(void* buffer, size_t bytes, int* dev_status, void* stream);
 PA_API int pa_calibration(int* num_sms, uint16_t* weights_out);
 PA_API void pa_calibration_clear(void);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The step around the attention: tables and slots from request lengths, rotary
+ * positions with the append, a cache held in 4 bits, verification of drafts.
+ * With these calls a step runs from lengths to accepted tokens without the
+ * host, and can be captured in a CUDA graph.
+ * ---------------------------------------------------------------------------
+ *
+ * pa_step_slots -- block tables, row offsets, positions and slots of a step,
+ * built on the GPU from request lengths ("vLLM serving internals",
+ * "PagedAttention as a virtual memory system": a sequence takes a block when
+ * its last one is full; a finished sequence's blocks return to the pool).  The
+ * host allocator's rules for unshared blocks, as one launch.
+ *
+ *   new_tokens   int32 [num_seqs]  > 0: rows the sequence adds this step;
+ *                                  0: none; < 0: it gives up its last
+ *                                  -new_tokens tokens (all of them: finished)
+ *   context_lens, blocks_held  int32 [num_seqs]  tokens stored and table
+ *                entries owned before the step.  A sequence may hold more blocks
+ *                than its tokens need (after rejected drafts); they are used
+ *                first.
+ *   block_tables int32 [num_seqs, max_blocks_per_seq]  new entries are written
+ *                behind the held ones; entries past the held count mean nothing
+ *   free_blocks  int32 [num_blocks]  the queue of free blocks, a ring; blocks
+ *                are taken at its head and returned at its tail (returned ones
+ *                are not taken in the same step)
+ *   free_state   int32 [2]  {place of the head, free blocks}
+ *
+ * Results: query_start int32 [num_seqs + 1] (sums of max(new_tokens, 0));
+ * positions and slot_mapping int32 [max_tokens], one per row, -1 in the rows
+ * behind the last sequence's; *_out the lengths, held counts and queue state
+ * after the step (each may be its input: updated in place).  Row i of sequence
+ * s has position context_lens[s] + i and the slot of that position.
+ *
+ * A sequence is served whole or not at all, in order: the first whose blocks
+ * the queue cannot cover and all later ones that need a block are refused
+ * (PA_ERR_NO_BLOCKS bit).  Refused too, with the RANGE bit: a sequence that
+ * would outgrow its table, whose rows would end past max_tokens, that gives up
+ * more tokens than it has, or whose lengths contradict each other.  A refused
+ * sequence's state stays as it was; its rows keep their place in query_start
+ * and get position and slot -1.  A bad queue state or a bad block ID sets the
+ * RANGE bit; the slot is -1 then.  Blocks shared between sequences are the host
+ * allocator's: do not give them up here.  block_size 16 or 32;
+ * num_blocks * block_size and max_blocks_per_seq * block_size fit in int32.
+ */
+PA_API int pa_step_slots(const int32_t* new_tokens, const int32_t* context_lens, int32_t* context_lens_out,
+                         const int32_t* blocks_held, int32_t* blocks_held_out, int32_t* block_tables,
+                         int max_blocks_per_seq, int32_t* free_blocks, const int32_t* free_state,
+                         int32_t* free_state_out, int num_seqs, int num_blocks, int block_size, int32_t* query_start,
+                         int32_t* positions, int32_t* slot_mapping, int max_tokens, int* dev_status, void* stream);
+
+/*
+ * pa_rope_table -- cosines and sines of rotary positions: row p of table
+ * (float [table_len, rot_dim]) holds m cos(p w_i) for the rot_dim / 2 pairs,
+ * then m sin(p w_i).  w_i = base^(-2 i / rot_dim), scaled for contexts longer
+ * than the model was trained on:
+ *   PA_ROPE_PLAIN   w_i
+ *   PA_ROPE_LINEAR  w_i / factor (positions squeezed)
+ *   PA_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   PA_ROPE_YARN    w_i for pairs that turn more than `high` (32) times within
+ *                   original_positions, w_i / factor below `low` (1) turns, a
+ *                   ramp over the pair's index between; m = 0.1 ln(factor) + 1
+ *   PA_ROPE_BANDS   w_i over `high` (4) turns, w_i / factor under `low` (1), a
+ *                   ramp over the number of turns between
+ * scaling NULL means PLAIN.  attention_factor > 0 replaces m (0: the default of
+ * the type, 1 except for YARN).  Angles are taken in binary64.  rot_dim: a
+ * multiple of 16, at most 256.  Errors: PA_ERR_SHAPE for parameters that are not
+ * positive and finite or low >= high, PA_ERR_UNSUPPORTED for rot_dim or type.
+ */
+typedef enum {
+  PA_ROPE_PLAIN = 0,
+  PA_ROPE_LINEAR = 1,
+  PA_ROPE_NTK = 2,
+  PA_ROPE_YARN = 3,
+  PA_ROPE_BANDS = 4
+} pa_rope_type;
+typedef struct pa_rope_scaling {
+  int32_t type;
+  int32_t original_positions;
+  double factor;
+  double low;
+  double high;
+  double attention_factor;
+} pa_rope_scaling;
+PA_API int pa_rope_table(float* table, int table_len, int rot_dim, double base, const pa_rope_scaling* scaling,
+                         void* stream);
+
+/*
+ * pa_rope_append -- rotate a step's q and k to their positions; q goes to
+ * q_out, k and v into their cache slots (pa_cache_append's contract for
+ * slot_mapping).  One launch in place of a rotation of q, one of k and an
+ * append.
+ *
+ * The first rot_dim dims of each q and k head turn: a pair (x, y) becomes
+ * (x c - y s, y c + x s) with (c, s) from row positions[t] of the table, the
+ * exact value rounded once to bf16.  Pairs are dims (i, i + rot_dim / 2), or
+ * (2 i, 2 i + 1) with `interleaved`.  The other dims pass unchanged.
+ *
+ * q, k_new, v_new: bf16 [num_tokens, heads, head_dim] whose tokens lie
+ * *_stride elements apart (views of one projection's output; a multiple of 8,
+ * at least heads * head_dim).  q_out is contiguous and may be q itself.
+ * positions[t] < 0: padding, nothing of row t is written.  positions[t] >=
+ * table_len: likewise, with the RANGE bit.  slot < 0: q is rotated, k and v are
+ * not stored; a slot past the pool: likewise, with the RANGE bit.  rot_dim: a
+ * multiple of 16 up to head_dim; table 16-byte aligned.  Any number of heads.
+ *
+ * _fp8 and _int4 store into those caches: the codes are those that
+ * pa_cache_append_fp8 / pa_cache_append_int4 give for the rotated bf16 rows.
+ */
+PA_API int pa_rope_append(void* q_out, const void* q, long long q_stride, const void* k_new, long long k_stride,
+                          const void* v_new, long long v_stride, void* k_cache, void* v_cache, const float* table,
+                          int table_len, int rot_dim, int interleaved, const int32_t* positions,
+                          const int32_t* slot_mapping, int num_tokens, int num_blocks, int num_q_heads,
+                          int num_kv_heads, int head_dim, int block_size, int* dev_status, void* stream);
+PA_API int pa_rope_append_fp8(void* q_out, const void* q, long long q_stride, const void* k_new, long long k_stride,
+                              const void* v_new, long long v_stride, void* k_cache, void* v_cache,
+                              const float* table, int table_len, int rot_dim, int interleaved,
+                              const int32_t* positions, const int32_t* slot_mapping, int num_tokens, int num_blocks,
+                              int num_q_heads, int num_kv_heads, int head_dim, int block_size, float k_scale,
+                              float v_scale, int* dev_status, void* stream);
+PA_API int pa_rope_append_int4(void* q_out, const void* q, long long q_stride, const void* k_new, long long k_stride,
+                               const void* v_new, long long v_stride, void* k_cache, void* v_cache,
+                               const float* table, int table_len, int rot_dim, int interleaved,
+                               const int32_t* positions, const int32_t* slot_mapping, int num_tokens, int num_blocks,
+                               int num_q_heads, int num_kv_heads, int head_dim, int block_size, int* dev_status,
+                               void* stream);
+
+/*
+ * A cache held in 4 bits.  Each 32 consecutive dims of a row have one fp16
+ * scale s = fp16(max|x| / 7) (at most 65504) and codes u = 8 + round(x / s),
+ * nearest even, kept in 1 .. 15; value = (u - 8) * s.  9/16 byte per value, 28 % of
+ * bf16's and 56 % of E4M3's, with no scale to choose.  A NaN makes the 32
+ * dims it is in NaN; infinities become the largest value of their scale.
+ * k_cache / v_cache: uint8 [num_blocks, num_kv_heads, block_size,
+ * head_dim * 9/16].  Within one (block, head): the rows' codes, head_dim / 2
+ * bytes each, then the rows' scales, head_dim / 32 fp16 each.  16 bytes of codes
+ * hold 32 dims: byte 2 i + h has dims i + 16 h (low nibble) and i + 16 h + 8;
+ * with n = head_dim / 32, the 16 bytes of chunk c of row r (within its block)
+ * stand at place c XOR ((r / (8 / n)) mod n) of the row.
+ *
+ * pa_cache_append_int4 -- pa_cache_append into such a cache (quantising).
+ * pa_cache_read_int4   -- the rows in the given slots as values: k_out, v_out
+ *   float [num_tokens, num_kv_heads, head_dim] (exact).  Rows of negative slots
+ *   are left as they are; a slot past the pool too, with the RANGE bit.  For
+ *   moving a prefix to another cache or engine.
+ */
+PA_API int pa_cache_append_int4(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                                const int32_t* slot_mapping, int num_tokens, int num_blocks, int num_kv_heads,
+                                int head_dim, int block_size, int* dev_status, void* stream);
+PA_API int pa_cache_read_int4(float* k_out, float* v_out, const void* k_cache, const void* v_cache,
+                              const int32_t* slot_mapping, int num_tokens, int num_blocks, int num_kv_heads,
+                              int head_dim, int block_size, int* dev_status, void* stream);
+
+/*
+ * pa_decode_int4 / pa_prefill_chunk_int4 -- pa_decode and pa_prefill_chunk over
+ * a 4-bit cache: the same arguments, shapes (head_dim 64, 128, 256) and results
+ * up to rounding.  The append is a call of its own (pa_rope_append_int4,
+ * pa_cache_append_int4).  Rows of q behind query_start[num_seqs] are not read
+ * and their output is left as it was.  Keys in a bad block are skipped, with the
+ * RANGE bit.
+ *
+ * pa_int4_workspace_bytes: bytes of workspace on the CURRENT device, for any
+ * batch of these heads; contract of pa_workspace_bytes (zero-filled once, one
+ * workspace per call in flight).  Returns 0 for invalid sizes.
+ */
+PA_API size_t pa_int4_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim);
+PA_API int pa_decode_int4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                          int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                          int num_blocks, float scale, void* workspace, size_t workspace_bytes, int* dev_status,
+                          void* stream);
+PA_API int pa_prefill_chunk_int4(void* out, const void* q, const int32_t* query_start, const void* k_cache,
+                                 const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* context_lens, int num_seqs, int total_q_tokens, int num_q_heads,
+                                 int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+                                 void* workspace, size_t workspace_bytes, int* dev_status, void* stream);
+
+/*
+ * pa_accept_drafts -- which drafted tokens a verification step keeps, and the
+ * token that follows them ("Inference optimization", section "Speculative
+ * decoding": the accepted tokens are distributed as the target's).
+ *
+ * Sequence s has rows query_start[s] .. query_start[s+1]-1 of the batch that
+ * pa_prefill_chunk attended to: row 0 its newest token, the others its drafts.
+ * tokens[r] int32 is the token fed at row r; row r + 1's was drawn from row r of
+ * draft_probs [total_rows, vocab] (a sequence's last draft row is not read).
+ * target_probs [total_rows, vocab] are the target's probabilities after each
+ * row.  Both are float, or bf16 with probs_bf16 = 1; rows lie *_stride elements
+ * apart.  draft_probs NULL: the drafts were looked up, not drawn (probability 1).
+ * uniforms float [total_rows], in [0, 1).
+ *
+ *   draft of row r + 1, token d: kept if uniforms[r] * draft[r][d] < target[r][d]
+ *   and all drafts before it are kept.  A negative token ends the drafts there
+ *   (fewer drafts than rows); one past the vocabulary too, with the RANGE bit.
+ *   After a refusal at row r the weights are max(target[r] - draft[r], 0)
+ *   (draft NULL: target[r] without the refused token); if they are all zero, or
+ *   no draft was refused, the target row's own.  With the last row's uniform u
+ *   the new token is the lowest index whose running sum of weights passes
+ *   u * (their sum); weights that are negative, infinite or NaN count as zero.
+ *   Sums and products are taken in binary64.
+ *
+ * Results: num_accepted int32 [num_seqs]; out_tokens int32 [total_rows]: each
+ * sequence's kept drafts, the new token, then -1.  A row without any weight
+ * gives -1 and the RANGE bit.  With context_lens / context_lens_out int32
+ * [num_seqs] (may be the same; NULL: neither) the lengths lose the rows that
+ * were not kept: the next step's lengths before its new token is added.  A
+ * sequence without rows keeps nothing and loses nothing; a query_start outside
+ * [0, total_rows] likewise, with the RANGE bit.  Rows of out_tokens outside
+ * every sequence are left as they were.
+ */
+PA_API int pa_accept_drafts(int32_t* out_tokens, int32_t* num_accepted, const void* target_probs,
+                            long long target_stride, const void* draft_probs, long long draft_stride, int probs_bf16,
+                            const int32_t* tokens, const int32_t* query_start, const float* uniforms, int num_seqs,
+                            int total_rows, int vocab, const int32_t* context_lens, int32_t* context_lens_out,
+                            int* dev_status, void* stream);
 
 /* Human-readable name of a pa_status value (static storage). */
 PA_API const char* pa_status_string(int status);

@@ -16,6 +16,9 @@ __all__ = [
     "pa_status_string", "pa_last_cuda_error", "pa_last_cuda_error_string", "PAError", "library_path",
     "make_workspace", "status_bit", "pa_plan_batch", "pa_prefill_chunk_planned", "Plan",
     "pa_calibrate", "pa_calibration", "pa_calibration_clear", "pa_prefill_chunk_fp8",
+    "pa_step_slots", "pa_rope_table", "pa_rope_append", "pa_rope_append_fp8", "pa_rope_append_int4",
+    "pa_cache_append_int4", "pa_cache_read_int4", "pa_int4_workspace_bytes", "make_int4_workspace", "pa_decode_int4",
+    "pa_prefill_chunk_int4", "pa_accept_drafts",
 ]
 
 

@@ -78,9 +78,44 @@ _lib.pa_last_cuda_error.restype = _ci
 _lib.pa_last_cuda_error_string.argtypes = []
 _lib.pa_last_cuda_error_string.restype = ctypes.c_char_p
 
+_ll, _cf, _cd = ctypes.c_longlong, ctypes.c_float, ctypes.c_double
+
+
+class RopeScaling(ctypes.Structure):
+    """pa_rope_scaling: how rotary frequencies are scaled for long contexts."""
+    _fields_ = [("type", ctypes.c_int32), ("original_positions", ctypes.c_int32), ("factor", _cd), ("low", _cd),
+                ("high", _cd), ("attention_factor", _cd)]
+
+
+_lib.pa_step_slots.argtypes = [_i32p] * 6 + [_ci] + [_i32p] * 3 + [_ci] * 3 + [_i32p] * 3 + [_ci, _vp, _vp]
+_lib.pa_step_slots.restype = _ci
+_lib.pa_rope_table.argtypes = [_vp, _ci, _ci, _cd, ctypes.POINTER(RopeScaling), _vp]
+_lib.pa_rope_table.restype = _ci
+_rope_args = [_vp, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ci, _ci, _ci, _i32p, _i32p] + [_ci] * 6
+_lib.pa_rope_append.argtypes = _rope_args + [_vp, _vp]
+_lib.pa_rope_append.restype = _ci
+_lib.pa_rope_append_fp8.argtypes = _rope_args + [_cf, _cf, _vp, _vp]
+_lib.pa_rope_append_fp8.restype = _ci
+_lib.pa_rope_append_int4.argtypes = _rope_args + [_vp, _vp]
+_lib.pa_rope_append_int4.restype = _ci
+_lib.pa_cache_append_int4.argtypes = [_vp, _vp, _vp, _vp, _i32p, _ci, _ci, _ci, _ci, _ci, _vp, _vp]
+_lib.pa_cache_append_int4.restype = _ci
+_lib.pa_cache_read_int4.argtypes = [_vp, _vp, _vp, _vp, _i32p, _ci, _ci, _ci, _ci, _ci, _vp, _vp]
+_lib.pa_cache_read_int4.restype = _ci
+_lib.pa_int4_workspace_bytes.argtypes = [_ci, _ci, _ci]
+_lib.pa_int4_workspace_bytes.restype = ctypes.c_size_t
+_lib.pa_decode_int4.argtypes = _lib.pa_decode.argtypes
+_lib.pa_decode_int4.restype = _ci
+_lib.pa_prefill_chunk_int4.argtypes = _lib.pa_prefill_chunk.argtypes
+_lib.pa_prefill_chunk_int4.restype = _ci
+_lib.pa_accept_drafts.argtypes = [_i32p, _i32p, _vp, _ll, _vp, _ll, _ci, _i32p, _i32p, _vp, _ci, _ci, _ci, _i32p,
+                                  _i32p, _vp, _vp]
+_lib.pa_accept_drafts.restype = _ci
+
 PA_OK = 0
 PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE = -1, -2, -3, -4
 PA_ERR_RANGE, PA_ERR_CUDA, PA_ERR_TIMEOUT = -5, -6, -7
+PA_ERR_NO_BLOCKS = -8
 STATIC_SCRATCH_BYTES = 64 * 1024 * 1024  # PA_STATIC_SCRATCH_BYTES of include/pa.h
 
 
@@ -442,9 +477,266 @@ def pa_decode_static_scratch(out, q, k_cache, v_cache, block_tables, context_len
     _check(rc)
 
 
+# ---- the step around the attention -------------------------------------------------
+class _Args:
+    """Checks the tensors of one call and collects their device: all on one
+    CUDA device, which is made current for the launch if it is not."""
+    __slots__ = ("device",)
+
+    def __init__(self, first):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise ValueError("the tensors must be on a CUDA device")
+        self.device = first.get_device()
+
+    def ptr(self, t, name, dtype, shape, strided=False):
+        """Device pointer of t, which must have this dtype and shape (None: any
+        extent) and be contiguous -- or, strided, contiguous in all but its first dimension."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} must be on the CUDA device of the call's other tensors")
+        got = t.shape
+        if len(got) != len(shape) or any(n is not None and n != g for n, g in zip(shape, got)):
+            raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, "
+                             f"got {tuple(got)}")
+        if not t.is_contiguous() and not (strided and (got[0] == 0 or t[0].is_contiguous())):
+            raise ValueError(f"{name} must be contiguous" + (" within each row" if strided else ""))
+        return t.data_ptr()
+
+    def status(self, dev_status):
+        if dev_status is None:
+            return None
+        return self.ptr(dev_status, "dev_status", torch.int32, (1,))
+
+    def call(self, fn, stream, *args):
+        """fn(*args, stream) with the tensors' device current, on `stream` or that device's current one."""
+        if torch.cuda.current_device() == self.device:
+            s = torch.cuda.current_stream().cuda_stream if stream is None else _stream_ptr(stream)
+            rc = fn(*args, s)
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, _stream_ptr(stream))
+        if rc != PA_OK:
+            _check(rc)
+
+
+def _row_stride(t, width):
+    """Elements from one row of t to the next (a single row's stride means nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def pa_step_slots(new_tokens, context_lens, blocks_held, block_tables, free_blocks, free_state, block_size,
+                  query_start, positions, slot_mapping, context_lens_out=None, blocks_held_out=None,
+                  free_state_out=None, dev_status=None, stream=None) -> None:
+    """Block tables, row offsets, positions and slots of a step from request
+    lengths, all int32 on the GPU; see include/pa.h.  new_tokens, context_lens,
+    blocks_held [B], block_tables [B, max_blocks], free_blocks [num_blocks],
+    free_state [2] (head, count); query_start [B + 1], positions and
+    slot_mapping [max_tokens] are written.  The lengths, held counts and queue
+    state are updated in place unless other outputs are given."""
+    if context_lens_out is None:
+        context_lens_out = context_lens
+    if blocks_held_out is None:
+        blocks_held_out = blocks_held
+    if free_state_out is None:
+        free_state_out = free_state
+    a, i32 = _Args(new_tokens), torch.int32
+    b = new_tokens.shape[0] if new_tokens.dim() else 0
+    t = positions.shape[0] if isinstance(positions, torch.Tensor) and positions.dim() else 0
+    a.call(_lib.pa_step_slots, stream, a.ptr(new_tokens, "new_tokens", i32, (b,)),
+           a.ptr(context_lens, "context_lens", i32, (b,)), a.ptr(context_lens_out, "context_lens_out", i32, (b,)),
+           a.ptr(blocks_held, "blocks_held", i32, (b,)), a.ptr(blocks_held_out, "blocks_held_out", i32, (b,)),
+           a.ptr(block_tables, "block_tables", i32, (b, None)), block_tables.shape[1],
+           a.ptr(free_blocks, "free_blocks", i32, (None,)), a.ptr(free_state, "free_state", i32, (2,)),
+           a.ptr(free_state_out, "free_state_out", i32, (2,)), b, free_blocks.shape[0], int(block_size),
+           a.ptr(query_start, "query_start", i32, (b + 1,)), a.ptr(positions, "positions", i32, (t,)),
+           a.ptr(slot_mapping, "slot_mapping", i32, (t,)), t, a.status(dev_status))
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}  # pa_rope_type of include/pa.h
+
+
+def pa_rope_table(table, base=10000.0, scaling="none", factor=1.0, original_positions=0, low=None, high=None,
+                  attention_factor=0.0, stream=None) -> None:
+    """Fill table [positions, rot_dim] (float32) with the cosines, then the
+    sines, of rotary positions; scaling: "none", "linear", "ntk", "yarn" or
+    "bands" (low and high default to 1 and 32, for bands 1 and 4).  See
+    include/pa.h."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    a = _Args(table)
+    p = a.ptr(table, "table", torch.float32, (None, None))
+    sc = RopeScaling(ROPE_SCALINGS[scaling], int(original_positions), float(factor), 1.0 if low is None else float(low),
+                     (4.0 if scaling == "bands" else 32.0) if high is None else float(high), float(attention_factor))
+    a.call(_lib.pa_rope_table, stream, p, table.shape[0], table.shape[1], float(base), ctypes.byref(sc))
+
+
+def _rope_call(fn, cache_dtype, cache_width, q_out, q, k_new, v_new, k_cache, v_cache, table, positions, slot_mapping,
+               interleaved, scales, dev_status, stream):
+    a, bf, i32 = _Args(q), torch.bfloat16, torch.int32
+    if q.dim() != 3 or not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
+        raise ValueError("q must be [T, Hq, d] and k_new [T, Hkv, d]")
+    t, hq, d = q.shape
+    hkv = k_new.shape[1]
+    kc = a.ptr(k_cache, "k_cache", cache_dtype, (None, hkv, None, cache_width(d)))
+    a.call(fn, stream, a.ptr(q_out, "q_out", bf, (t, hq, d)), a.ptr(q, "q", bf, (t, hq, d), True),
+           _row_stride(q, hq * d), a.ptr(k_new, "k_new", bf, (t, hkv, d), True), _row_stride(k_new, hkv * d),
+           a.ptr(v_new, "v_new", bf, (t, hkv, d), True), _row_stride(v_new, hkv * d), kc,
+           a.ptr(v_cache, "v_cache", cache_dtype, tuple(k_cache.shape)),
+           a.ptr(table, "table", torch.float32, (None, None)), table.shape[0], table.shape[1], 1 if interleaved else 0,
+           a.ptr(positions, "positions", i32, (t,)), a.ptr(slot_mapping, "slot_mapping", i32, (t,)), t,
+           k_cache.shape[0], hq, hkv, d, k_cache.shape[2], *scales, a.status(dev_status))
+
+
+def _int4_width(d):
+    """Bytes of a head's row of d values in a 4-bit cache: codes and scales."""
+    return d * 9 // 16
+
+
+def pa_rope_append(q_out, q, k_new, v_new, k_cache, v_cache, table, positions, slot_mapping, interleaved=False,
+                   dev_status=None, stream=None) -> None:
+    """Rotate q [T, Hq, d] into q_out and k_new [T, Hkv, d] into the bf16 cache
+    by table row positions[t]; v_new goes to the cache unrotated.  q, k_new and
+    v_new may be views of one projection's output (contiguous within a token);
+    q_out may be q.  See include/pa.h."""
+    _rope_call(_lib.pa_rope_append, torch.bfloat16, lambda d: d, q_out, q, k_new, v_new, k_cache, v_cache, table,
+               positions, slot_mapping, interleaved, (), dev_status, stream)
+
+
+def pa_rope_append_fp8(q_out, q, k_new, v_new, k_cache, v_cache, table, positions, slot_mapping, k_scale, v_scale,
+                       interleaved=False, dev_status=None, stream=None) -> None:
+    """pa_rope_append into an FP8 (E4M3 codes, uint8) cache with per-tensor scales."""
+    _rope_call(_lib.pa_rope_append_fp8, torch.uint8, lambda d: d, q_out, q, k_new, v_new, k_cache, v_cache, table,
+               positions, slot_mapping, interleaved, (float(k_scale), float(v_scale)), dev_status, stream)
+
+
+def pa_rope_append_int4(q_out, q, k_new, v_new, k_cache, v_cache, table, positions, slot_mapping, interleaved=False,
+                        dev_status=None, stream=None) -> None:
+    """pa_rope_append into a 4-bit cache (uint8 [num_blocks, Hkv, block_size, d * 9 / 16])."""
+    _rope_call(_lib.pa_rope_append_int4, torch.uint8, _int4_width, q_out, q, k_new, v_new, k_cache, v_cache, table,
+               positions, slot_mapping, interleaved, (), dev_status, stream)
+
+
+def pa_cache_append_int4(k_new, v_new, k_cache, v_cache, slot_mapping, dev_status=None, stream=None) -> None:
+    """Quantise k_new / v_new [T, Hkv, d] (bf16) into a 4-bit cache (uint8
+    [num_blocks, Hkv, block_size, d * 9 / 16]) at slot_mapping [T]; see include/pa.h."""
+    a, bf = _Args(k_new), torch.bfloat16
+    if k_new.dim() != 3:
+        raise ValueError("k_new must be [T, Hkv, d]")
+    t, hkv, d = k_new.shape
+    kc = a.ptr(k_cache, "k_cache", torch.uint8, (None, hkv, None, _int4_width(d)))
+    a.call(_lib.pa_cache_append_int4, stream, a.ptr(k_new, "k_new", bf, (t, hkv, d)),
+           a.ptr(v_new, "v_new", bf, (t, hkv, d)), kc, a.ptr(v_cache, "v_cache", torch.uint8, tuple(k_cache.shape)),
+           a.ptr(slot_mapping, "slot_mapping", torch.int32, (t,)), t, k_cache.shape[0], hkv, d, k_cache.shape[2],
+           a.status(dev_status))
+
+
+def pa_cache_read_int4(k_out, v_out, k_cache, v_cache, slot_mapping, dev_status=None, stream=None) -> None:
+    """The rows of a 4-bit cache in slot_mapping [T] as values: k_out / v_out
+    [T, Hkv, d] (float32); rows of negative slots are left as they are."""
+    a, f = _Args(k_out), torch.float32
+    if k_out.dim() != 3:
+        raise ValueError("k_out must be [T, Hkv, d]")
+    t, hkv, d = k_out.shape
+    kc = a.ptr(k_cache, "k_cache", torch.uint8, (None, hkv, None, _int4_width(d)))
+    a.call(_lib.pa_cache_read_int4, stream, a.ptr(k_out, "k_out", f, (t, hkv, d)),
+           a.ptr(v_out, "v_out", f, (t, hkv, d)), kc, a.ptr(v_cache, "v_cache", torch.uint8, tuple(k_cache.shape)),
+           a.ptr(slot_mapping, "slot_mapping", torch.int32, (t,)), t, k_cache.shape[0], hkv, d, k_cache.shape[2],
+           a.status(dev_status))
+
+
+def pa_int4_workspace_bytes(num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    n = int(_lib.pa_int4_workspace_bytes(num_q_heads, num_kv_heads, head_dim))
+    if n == 0:
+        raise PAError(PA_ERR_UNSUPPORTED)
+    return n
+
+
+def make_int4_workspace(num_q_heads: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """A zero-filled workspace for pa_decode_int4 / pa_prefill_chunk_int4 (the zero fill is required once)."""
+    with torch.cuda.device(device):  # None: the current device
+        n = pa_int4_workspace_bytes(num_q_heads, num_kv_heads, head_dim)
+        return torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+
+def _int4_attention(fn, out, q, query_start, k_cache, v_cache, block_tables, context_lens, scale, workspace,
+                    dev_status, stream):
+    a, i32 = _Args(q), torch.int32
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, Hq, d]")
+    t, hq, d = q.shape
+    b = context_lens.shape[0] if isinstance(context_lens, torch.Tensor) and context_lens.dim() else 0
+    head = (a.ptr(out, "out", torch.bfloat16, (t, hq, d)), a.ptr(q, "q", torch.bfloat16, (t, hq, d)))
+    rows = ()
+    if query_start is not None:
+        head += (a.ptr(query_start, "query_start", i32, (b + 1,)),)
+        rows = (t,)
+    elif t != b:
+        raise ValueError("pa_decode_int4 takes exactly one query row per sequence")
+    kc = a.ptr(k_cache, "k_cache", torch.uint8, (None, None, None, _int4_width(d)))
+    nb, hkv, bs, _ = k_cache.shape
+    a.call(fn, stream, *head, kc, a.ptr(v_cache, "v_cache", torch.uint8, (nb, hkv, bs, _int4_width(d))),
+           a.ptr(block_tables, "block_tables", i32, (b, None)), block_tables.shape[1],
+           a.ptr(context_lens, "context_lens", i32, (b,)), b, *rows, hq, hkv, d, bs, nb, float(scale),
+           a.ptr(workspace, "workspace", torch.uint8, (None,)), workspace.shape[0], a.status(dev_status))
+
+
+def pa_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, scale, workspace, dev_status=None,
+                   stream=None) -> None:
+    """pa_decode over a 4-bit cache (uint8 [num_blocks, Hkv, block_size, d * 9 / 16]); see include/pa.h."""
+    _int4_attention(_lib.pa_decode_int4, out, q, None, k_cache, v_cache, block_tables, context_lens, scale, workspace,
+                    dev_status, stream)
+
+
+def pa_prefill_chunk_int4(out, q, query_start, k_cache, v_cache, block_tables, context_lens, scale, workspace,
+                          dev_status=None, stream=None) -> None:
+    """pa_prefill_chunk over a 4-bit cache, as pa_decode_int4."""
+    if query_start is None:
+        raise TypeError("query_start must be a torch.Tensor")
+    _int4_attention(_lib.pa_prefill_chunk_int4, out, q, query_start, k_cache, v_cache, block_tables, context_lens,
+                    scale, workspace, dev_status, stream)
+
+
+def pa_accept_drafts(out_tokens, num_accepted, target_probs, draft_probs, tokens, query_start, uniforms,
+                     context_lens=None, context_lens_out=None, dev_status=None, stream=None) -> None:
+    """Which drafted tokens a verification step keeps and the token after them:
+    target_probs [rows, vocab] and draft_probs (the same, or None: drafts that
+    were looked up) in float32 or bfloat16, tokens [rows] the token fed at each
+    row, query_start [B + 1], uniforms [rows] in [0, 1).  out_tokens [rows] and
+    num_accepted [B] are written; context_lens [B], if given, lose the rows not
+    kept (in place, or into context_lens_out).  See include/pa.h."""
+    a, i32 = _Args(target_probs), torch.int32
+    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("target_probs must be float32 or bfloat16")
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be [rows, vocab]")
+    r, v = target_probs.shape
+    b = num_accepted.shape[0] if isinstance(num_accepted, torch.Tensor) and num_accepted.dim() else 0
+    if context_lens is None and context_lens_out is not None:
+        raise ValueError("context_lens_out needs context_lens")
+    if context_lens_out is None:
+        context_lens_out = context_lens
+    dp, ds = None, 0
+    if draft_probs is not None:
+        dp = a.ptr(draft_probs, "draft_probs", target_probs.dtype, (r, v), True)
+        ds = _row_stride(draft_probs, v)
+    a.call(_lib.pa_accept_drafts, stream, a.ptr(out_tokens, "out_tokens", i32, (r,)),
+           a.ptr(num_accepted, "num_accepted", i32, (b,)),
+           a.ptr(target_probs, "target_probs", target_probs.dtype, (r, v), True), _row_stride(target_probs, v), dp, ds,
+           int(target_probs.dtype is torch.bfloat16), a.ptr(tokens, "tokens", i32, (r,)),
+           a.ptr(query_start, "query_start", i32, (b + 1,)), a.ptr(uniforms, "uniforms", torch.float32, (r,)), b, r, v,
+           None if context_lens is None else a.ptr(context_lens, "context_lens", i32, (b,)),
+           None if context_lens is None else a.ptr(context_lens_out, "context_lens_out", i32, (b,)),
+           a.status(dev_status))
+
+
 def exported_symbols() -> list[str]:
     return ["pa_cache_append", "pa_workspace_bytes", "pa_decode", "pa_decode_append", "pa_cache_append_fp8",
             "pa_decode_fp8", "pa_cascade_workspace_bytes", "pa_decode_cascade", "pa_prefill_chunk",
             "pa_decode_static_scratch", "pa_status_string", "pa_last_cuda_error", "pa_last_cuda_error_string",
             "pa_plan_batch", "pa_prefill_chunk_planned", "pa_prefill_chunk_fp8", "pa_calibrate_bytes", "pa_calibrate", "pa_calibration",
-            "pa_calibration_clear"]
+            "pa_calibration_clear", "pa_step_slots", "pa_rope_table", "pa_rope_append", "pa_rope_append_fp8",
+            "pa_rope_append_int4", "pa_cache_append_int4", "pa_cache_read_int4", "pa_int4_workspace_bytes",
+            "pa_decode_int4", "pa_prefill_chunk_int4", "pa_accept_drafts"]

@@ -604,6 +604,7 @@ const char* pa_status_string(int status) {
     case PA_ERR_RANGE: return "PA_ERR_RANGE: block ID, slot or context outside its table or pool";
     case PA_ERR_CUDA: return "PA_ERR_CUDA: a CUDA call failed";
     case PA_ERR_TIMEOUT: return "PA_ERR_TIMEOUT: a bounded device wait gave up";
+    case PA_ERR_NO_BLOCKS: return "PA_ERR_NO_BLOCKS: too few free blocks in the pool";
     default: return "unknown pa_status";
   }
 }
