@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(ACC_THREADS) accept_kernel(const AcceptParams 
     if (tid == 0) {
       p.num_accepted[s] = acc;
       if (p.context_lens) p.context_lens_out[s] = p.context_lens[s] - (rows - 1 - acc);
+      __threadfence();  // an attention kernel launched behind this one reads the lengths in its prologue
     }
   }
   if (owner < 0) {  // u times the total is not passed (rounding, u >= 1): the last token with a weight

@@ -5,8 +5,35 @@
 // table.  One pass over the keys with the running maximum and sum of the
 // softmax ("Inference optimization", "Build it -- Step 2").
 //
-// Simple form: one CTA per (query row, query head), its warps taking every
-// fourth key, a lane D / 32 dims.
+// The cache is read once: 2 D * 9/16 bytes per token and KV head, so HBM is the
+// floor; the unpacking of the codes (a dozen integer and fp16 instructions per
+// 8 codes with its share of the softmax) comes within sight of it, which is why
+// everything below counts instructions.
+//
+// Work: an item is (sequence, group of query rows, KV head); its columns are the
+// rows times the G query heads, 8 or 16 (NT n-tiles of 8).  Its keys are cut
+// into units of 32.  All units of the batch, in order, are cut into equal
+// contiguous ranges, one per CTA, and a CTA's range into one per warp; each
+// warp streams its own units through a ring of record copies (a record is one
+// contiguous run of bytes, so plain bulk copies bring it).
+//
+// Math, on fp16 warp MMAs with fp32 accumulators, keys or head dims in M and
+// the columns in N:
+//  - S = K q: a code becomes the fp16 number 256 + u or 16 + u by one mask-or
+//    (its nibble lands in the mantissa); the constant part, (256 + 8) or (16 + 8)
+//    times the sum of q over the dims, is the accumulator's starting value, so no
+//    instruction removes it.  A chunk's 32 dims share one scale: S += s * S_chunk.
+//  - q enters as fp16 scaled by a power of two per column (exact but for dims
+//    2^14 below the column's largest); the power is folded into the softmax scale.
+//  - the weights P = 2^(x - m) use a reference m that only moves when a score
+//    passes it, so a unit needs one vote and no lane exchange.  m sits one
+//    above the largest score seen: P <= 1, and fewer moves.
+//  - O += V^T P: the codes are made exact integers -7 .. 7 (one more subtraction:
+//    here a constant part would grow with the context and cost the sum its low
+//    bits); the chunk's scale, one per key, multiplies P (fp16, one rounding).
+// Pieces of an item cut between warps go to the workspace as (O, m, l); the
+// CTA merges those of its own warps, and the last CTA to bring a piece of an
+// item merges the CTAs', in order.  No thread waits for another CTA.
 #include "pa_device.cuh"
 #include "pa_int4.cuh"
 #include "pa_internal.h"
@@ -15,7 +42,23 @@ namespace pa {
 
 namespace {
 
-constexpr int I4_WARPS = 4;
+constexpr int I4_UNIT = 32;        // keys
+constexpr int I4_BUCKETS = 1024;   // prefix sums of the batch's units, of runs of sequences
+constexpr float I4_NO_MAX = -3e38f;
+
+template <int D, int NT>
+struct I4 {
+  static constexpr int NC = D / 32;                         // chunks of a row
+  static constexpr int COLS = 8 * NT;
+  static constexpr int WARPS = D * NT <= 128 ? 16 : 8;      // 128 or 255 registers a thread
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int HALF_BYTES = I4_UNIT * (D * 9 / 16); // K (or V) of a unit
+  static constexpr int STAGE_BYTES = 2 * HALF_BYTES;
+  static constexpr int STAGES = 221184 / WARPS / STAGE_BYTES;
+  static constexpr int PIECE = COLS * (D + 2);              // floats: O [COLS][D], m [COLS], l [COLS]
+  static constexpr int RING_BYTES = WARPS * STAGES * STAGE_BYTES;
+  static constexpr int SMEM = RING_BYTES + 8 * I4_BUCKETS + 8 * WARPS * STAGES + 512;
+};
 
 struct Int4Params {
   __nv_bfloat16* out;
@@ -25,85 +68,805 @@ struct Int4Params {
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* query_start;  // nullptr: one row per sequence
-  int num_seqs, num_rows, max_blocks, num_q_heads, num_kv_heads, group, block_shift, num_blocks;
+  int num_seqs, num_rows, max_blocks, num_q_heads, num_kv_heads, group, rows_per_item, block_shift, num_blocks;
   float scale_log2;
   int* status;
+  int* counters;        // workspace: pieces brought per CTA that an item starts in; zero between calls
+  float* warp_pieces;   // workspace: [CTA][warp][2]
+  float* cta_pieces;    // workspace: [CTA][2]
 };
 
-template <int D>
-__device__ __forceinline__ float int4_value(const uint8_t* rec, int bs, int r, int dim) {
-  const int c = dim >> 5, i = dim & 31;
-  const uint8_t b = rec[int4_code_offset<D>(r, c) + 2 * (i & 7) + (i >> 4)];
-  const float s = __half2float(*reinterpret_cast<const __half*>(rec + int4_scale_offset<D>(bs, r, c)));
-  return static_cast<float>(((b >> (4 * ((i >> 3) & 1))) & 15) - 8) * s;
+struct SeqInfo {
+  int q0, qlen, ctx, units;  // units of one item (0: no work), from the whole context
+};
+
+__device__ __forceinline__ SeqInfo i4_seq(const Int4Params& p, int s, int* bits = nullptr) {
+  SeqInfo i;
+  i.ctx = p.context_lens[s];
+  i.q0 = s;
+  i.qlen = 1;
+  int bad = 0;
+  if (p.query_start) {
+    i.q0 = p.query_start[s];
+    const int end = p.query_start[s + 1];
+    if (i.q0 < 0 || end < i.q0 || end > p.num_rows) {
+      bad = PA_STATUS_BIT(PA_ERR_RANGE);
+      i.q0 = 0;
+      i.qlen = 0;
+    } else {
+      i.qlen = end - i.q0;
+    }
+  }
+  if (i.ctx > p.max_blocks << p.block_shift) {
+    bad = PA_STATUS_BIT(PA_ERR_RANGE);
+    i.ctx = 0;
+  }
+  i.units = i.ctx > 0 && i.qlen > 0 ? (i.ctx + I4_UNIT - 1) / I4_UNIT : 0;
+  if (bits) *bits |= bad;
+  return i;
 }
 
-template <int D>
-__global__ void __launch_bounds__(32 * I4_WARPS) int4_simple_kernel(const Int4Params p) {
-  constexpr int N = D / 32;
-  __shared__ float sm[I4_WARPS], sl[I4_WARPS], so[I4_WARPS][D];
-  const int row = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int kh = h / p.group, bs = 1 << p.block_shift;
-  int s = row, keys;
-  if (p.query_start) {
-    int lo = 0, hi = p.num_seqs - 1;  // the sequence that owns the row
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.query_start[mid] <= row) lo = mid; else hi = mid - 1;
+__device__ __forceinline__ int i4_groups(const Int4Params& p, int qlen) {
+  return p.query_start ? (qlen + p.rows_per_item - 1) / p.rows_per_item : 1;
+}
+
+// A place in the batch's order of items: sequence, row group, KV head.
+struct Walk {
+  SeqInfo seq;
+  int s, rg, h;
+  int groups;
+  int live;  // units of the item that some row sees
+};
+
+__device__ __forceinline__ void i4_enter(const Int4Params& p, Walk& w) {
+  const int last = min((w.rg + 1) * p.rows_per_item, w.seq.qlen);  // rows of the item end here
+  const int keys = w.seq.ctx - w.seq.qlen + last;
+  w.live = keys > 0 ? (keys + I4_UNIT - 1) / I4_UNIT : 0;
+}
+
+__device__ __forceinline__ void i4_next(const Int4Params& p, Walk& w) {
+  if (++w.h == p.num_kv_heads) {
+    w.h = 0;
+    if (++w.rg == w.groups) {
+      w.rg = 0;
+      do {
+        if (++w.s >= p.num_seqs) return;  // the range ends before this is used
+        w.seq = i4_seq(p, w.s);
+      } while (w.seq.units == 0);
+      w.groups = i4_groups(p, w.seq.qlen);
     }
-    s = lo;
-    const int first = p.query_start[s], end = p.query_start[s + 1];
-    if (row == 0 && h == 0) {
-      for (int i = threadIdx.x; i < p.num_seqs; i += 32 * I4_WARPS)
-        if (p.query_start[i] < 0 || p.query_start[i + 1] < p.query_start[i] || p.query_start[i + 1] > p.num_rows)
-          set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
-    }
-    if (first < 0 || end > p.num_rows) return;
-    if (row < first || row >= end) return;  // behind the last sequence: left alone
-    keys = p.context_lens[s] - (p.query_start[s + 1] - row) + 1;
+    i4_enter(p, w);
+  }
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// 8 codes (nibbles of the two halves of w) -> 4 fp16 pairs: 256 + u in 0 and 2, 16 + u in 1 and 3.
+__device__ __forceinline__ void i4_expand(uint32_t w, uint32_t (&h)[4]) {
+  const uint32_t a = w << 2, b = w >> 6;
+  h[0] = (a & 0x003c003cu) | 0x5c005c00u;
+  h[1] = (a & 0x03c003c0u) | 0x4c004c00u;
+  h[2] = (b & 0x003c003cu) | 0x5c005c00u;
+  h[3] = (b & 0x03c003c0u) | 0x4c004c00u;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float half_of(uint32_t w, int hi) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(hi ? w >> 16 : w & 0xffff)));
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
   } else {
-    keys = p.context_lens[s];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
   }
-  if (keys > p.max_blocks << p.block_shift) {
-    if (threadIdx.x == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
-    keys = 0;
+}
+
+// Merge n pieces into one column: piece(k) is the k-th piece's record (or nullptr).  A warp
+// takes one column; lane i the dims 4 i .. 4 i + 3 of each 128.  If `final`,
+// writes the normalised row to out (bf16), else a piece record to dst.
+template <int D, int COLS, class Piece>
+__device__ __forceinline__ void merge_column(Piece piece, int n, int col, int lane, __nv_bfloat16* out, float* dst) {
+  float m = I4_NO_MAX;
+  for (int k = lane; k < n; k += 32) {
+    const float* r = piece(k);
+    if (r && __ldcg(r + COLS * (D + 1) + col) != 0.f) m = fmaxf(m, __ldcg(r + COLS * D + col));
   }
-  float q[N], o[N] = {}, m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    q[i] = __bfloat162float(p.q[(static_cast<long long>(row) * p.num_q_heads + h) * D + i * 32 + lane]);
-  for (int j = warp; j < keys; j += I4_WARPS) {
-    const int blk = p.block_tables[static_cast<long long>(s) * p.max_blocks + (j >> p.block_shift)];
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
-      continue;
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
+  constexpr int PARTS = (D + 127) / 128;
+  float4 acc[PARTS];
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float w = 0.f;
+    if (k0 + lane < n) {
+      const float* r = piece(k0 + lane);
+      const float lk = r ? __ldcg(r + COLS * (D + 1) + col) : 0.f;
+      if (lk != 0.f) {  // (a NaN sum stays)
+        w = fast_exp2(__ldcg(r + COLS * D + col) - m);
+        l += lk * w;
+      }
     }
-    const long long rec = (static_cast<long long>(blk) * p.num_kv_heads + kh) * int4_record_bytes(bs, D);
-    float dot = 0.f;
+    const int cnt = min(32, n - k0);
+    for (int k = 0; k < cnt; ++k) {
+      const float wk = __shfl_sync(FULL_MASK, w, k);
+      if (wk == 0.f) continue;
+      const float* r = piece(k0 + k) + col * D;
 #pragma unroll
-    for (int i = 0; i < N; ++i) dot += q[i] * int4_value<D>(p.k_cache + rec, bs, j & (bs - 1), i * 32 + lane);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) dot += __shfl_xor_sync(FULL_MASK, dot, x);
-    dot *= p.scale_log2;
-    const float mn = fmaxf(m, dot), a = exp2f(m - mn), w = exp2f(dot - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      o[i] = o[i] * a + w * int4_value<D>(p.v_cache + rec, bs, j & (bs - 1), i * 32 + lane);
+      for (int i = 0; i < PARTS; ++i)
+        if (D >= 128 || lane < D / 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(r + i * 128 + lane * 4));
+          acc[i].x += wk * x.x;
+          acc[i].y += wk * x.y;
+          acc[i].z += wk * x.z;
+          acc[i].w += wk * x.w;
+        }
+    }
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
 #pragma unroll
-  for (int i = 0; i < N; ++i) so[warp][i * 32 + lane] = o[i];
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(FULL_MASK, l, o);
+  if (out) {
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+      if (D >= 128 || lane < D / 4)
+        *reinterpret_cast<uint2*>(out + i * 128 + lane * 4) =
+            make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+  } else {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+      if (D >= 128 || lane < D / 4) *reinterpret_cast<float4*>(dst + col * D + i * 128 + lane * 4) = acc[i];
+    if (lane == 0) {
+      dst[COLS * D + col] = m;
+      dst[COLS * (D + 1) + col] = l;
+    }
+  }
+}
+
+// What a warp left behind, for the CTA's merge.
+struct WarpEnd {
+  // the item its range starts inside of (slot 0), and the one that starts in it and goes on (slot 1)
+  int has0, on0, has1;  // on0: slot 0's item goes on past the range
+  int row[2], rows[2], h[2];  // its first query row, its rows, its KV head
+  long long first[2];   // first unit of the item
+  int units[2];
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __grid_constant__ Int4Params p) {
+  using C = I4<D, NT>;
+  constexpr int NC = C::NC, COLS = C::COLS, WARPS = C::WARPS, STAGES = C::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
+  long long* prefix = reinterpret_cast<long long*>(smem + C::RING_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES + 8 * I4_BUCKETS);
+  __shared__ long long scan[WARPS];
+  __shared__ WarpEnd ends[WARPS];
+  __shared__ int sh_merge;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, qd = lane & 3;
+  const int bs = 1 << p.block_shift;
+
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(&bars[warp * STAGES + i], 1);
+    fence_mbar_init();
+  }
+
+  grid_dependency_wait();
+
+  // ---- units of the batch: prefix sums over runs of sequences
+  const int run = (p.num_seqs + I4_BUCKETS - 1) / I4_BUCKETS;
+  constexpr int PER = I4_BUCKETS / C::THREADS;
+  long long mine[PER], sum = 0;
+  int bits = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    for (int s = b * run; s < min((b + 1) * run, p.num_seqs); ++s) {
+      const SeqInfo q = i4_seq(p, s, &bits);
+      sum += static_cast<long long>(q.units) * i4_groups(p, q.qlen) * p.num_kv_heads;
+    }
+    mine[i] = sum;
+  }
+  if (bits && blockIdx.x == 0) set_status(p.status, bits);
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(FULL_MASK, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  float mm = -INFINITY, ll = 0.f;
-  for (int w = 0; w < I4_WARPS; ++w) mm = fmaxf(mm, sm[w]);
-  for (int w = 0; w < I4_WARPS; ++w) ll += sl[w] != 0.f ? sl[w] * exp2f(sm[w] - mm) : 0.f;
-  for (int d = threadIdx.x; d < D; d += 32 * I4_WARPS) {
-    float x = 0.f;
-    for (int w = 0; w < I4_WARPS; ++w) x += sl[w] != 0.f ? so[w][d] * exp2f(sm[w] - mm) : 0.f;
-    p.out[(static_cast<long long>(row) * p.num_q_heads + h) * D + d] = __float2bfloat16(ll != 0.f ? x / ll : 0.f);
+  long long before = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    before += w < warp ? scan[w] : 0;
+    total += scan[w];
   }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) prefix[tid * PER + i] = before + mine[i];  // inclusive
+  __syncthreads();
+
+  // rows without a key
+  const int row_vecs = p.num_q_heads * D / 8;
+  for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+    const SeqInfo q = i4_seq(p, s);
+    if (q.units == 0 && q.qlen > 0) {
+      uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<long long>(q.q0) * p.num_q_heads * D);
+      for (long long i = tid; i < static_cast<long long>(q.qlen) * row_vecs; i += C::THREADS)
+        o[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+
+  // ---- this CTA's and this warp's range: as few CTAs as give every warp a unit
+  const long long want = (total + WARPS - 1) / WARPS;
+  const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const auto cta_first = [&](long long c) { return c * (total / ctas) + (c < total % ctas ? c : total % ctas); };
+  const auto cta_of = [&](long long u) {
+    const long long q = total / ctas, r = total % ctas;
+    return static_cast<int>(u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q);
+  };
+  const long long c0 = cta_first(blockIdx.x), cn = cta_first(blockIdx.x + 1) - c0;
+  // (rounded up: warp 0 always has a unit)
+  const long long u0 = c0 + (warp * cn + WARPS - 1) / WARPS, u1 = c0 + ((warp + 1) * cn + WARPS - 1) / WARPS;
+  float* piece0 = p.warp_pieces + (static_cast<long long>(blockIdx.x) * WARPS + warp) * 2 * C::PIECE;
+
+  // column constants: column g + 8 nt of the B operand, columns 2 qd and 2 qd + 1 of the accumulators
+  int rowB[NT], headB[NT], rowA[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int c = nt * 8 + g;
+    rowB[nt] = c / p.group;
+    headB[nt] = c - rowB[nt] * p.group;
+    rowA[nt][0] = (nt * 8 + 2 * qd) / p.group;
+    rowA[nt][1] = (nt * 8 + 2 * qd + 1) / p.group;
+  }
+  // ldmatrix: lane i gives row (i & 7) + 8 ((i >> 3) & 1) of chunk i >> 4 (+ 2 per step)
+  const int lrow = (lane & 7) + (lane & 8);
+  const uint32_t code_at = int4_code_offset<D>(lrow, lane >> 4);
+  uint8_t* ring = smem + warp * STAGES * C::STAGE_BYTES;
+  uint64_t* bar = bars + warp * STAGES;
+  const uint64_t policy = policy_evict_first();
+  const int rec = int4_record_bytes(bs, D);
+  const int blocks_per_unit = I4_UNIT >> p.block_shift;  // 2 or 1
+
+  WarpEnd end{};
+  if (u0 < u1) {
+    // ---- find the item of u0
+    Walk w;
+    long long base;  // first unit of the item
+    {
+      int lo = 0, hi = I4_BUCKETS - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] > u0) hi = mid; else lo = mid + 1;
+      }
+      long long at = lo > 0 ? prefix[lo - 1] : 0;
+      int s = lo * run;
+      for (;; ++s) {
+        w.seq = i4_seq(p, s);
+        w.groups = i4_groups(p, w.seq.qlen);
+        const long long n = static_cast<long long>(w.seq.units) * w.groups * p.num_kv_heads;
+        if (at + n > u0) break;
+        at += n;
+      }
+      const long long item = (u0 - at) / w.seq.units;
+      w.s = s;
+      w.rg = static_cast<int>(item / p.num_kv_heads);
+      w.h = static_cast<int>(item - static_cast<long long>(w.rg) * p.num_kv_heads);
+      base = at + item * w.seq.units;
+      i4_enter(p, w);
+    }
+    // ---- producer: the same walk, ahead by up to STAGES units
+    Walk pw = w;
+    long long pbase = base;
+    int pu = static_cast<int>(u0 - base);
+    int pend = static_cast<int>(min(static_cast<long long>(w.live), u1 - base));
+    int ids = 0, ids_from = INT32_MAX;  // block IDs of 32 table entries from ids_from on, one per lane
+    int pstage = 0, flying = 0;  // flying: units loaded and not yet waited for
+    unsigned bad = 0;  // two bits per stage: blocks of its unit that were not loaded
+
+    const auto produce = [&]() {
+      while (pu >= pend) {
+        if (pbase + pw.seq.units >= u1) return;
+        pbase += pw.seq.units;
+        i4_next(p, pw);
+        pu = 0;
+        pend = static_cast<int>(min(static_cast<long long>(pw.live), u1 - pbase));
+        ids_from = INT32_MAX;
+      }
+      const int entry = pu * blocks_per_unit;
+      const int entries = (pw.seq.ctx + bs - 1) >> p.block_shift;
+      if (entry < ids_from || entry + blocks_per_unit > ids_from + 32) {
+        ids_from = entry;
+        ids = entry + lane < entries
+                  ? __ldg(p.block_tables + static_cast<long long>(pw.s) * p.max_blocks + entry + lane)
+                  : -1;
+      }
+      const int id0 = __shfl_sync(FULL_MASK, ids, entry - ids_from);
+      const int id1 = blocks_per_unit == 2 ? __shfl_sync(FULL_MASK, ids, entry + 1 - ids_from) : 0;
+      const bool in1 = blocks_per_unit == 2 && entry + 1 < entries;
+      const bool ok0 = id0 >= 0 && id0 < p.num_blocks, ok1 = in1 && id1 >= 0 && id1 < p.num_blocks;
+      unsigned b = 0;
+      if (!ok0 || (in1 && !ok1)) {
+        b = blocks_per_unit == 1 ? 3u : (ok0 ? 0u : 1u) | (in1 && !ok1 ? 2u : 0u);
+        if (lane == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
+      }
+      bad = (bad & ~(3u << (2 * pstage))) | (b << (2 * pstage));
+      if (lane == 0) {
+        uint8_t* dst = ring + pstage * C::STAGE_BYTES;
+        uint64_t* fb = bar + pstage;
+        mbar_arrive_expect_tx(fb, 2 * rec * ((ok0 ? 1 : 0) + (ok1 ? 1 : 0)));
+        if (ok0) {
+          const long long at = (static_cast<long long>(id0) * p.num_kv_heads + pw.h) * rec;
+          bulk_load(dst, p.k_cache + at, rec, fb, policy);
+          bulk_load(dst + C::HALF_BYTES, p.v_cache + at, rec, fb, policy);
+        }
+        if (ok1) {
+          const long long at = (static_cast<long long>(id1) * p.num_kv_heads + pw.h) * rec;
+          bulk_load(dst + rec, p.k_cache + at, rec, fb, policy);
+          bulk_load(dst + C::HALF_BYTES + rec, p.v_cache + at, rec, fb, policy);
+        }
+      }
+      if (++pstage == STAGES) pstage = 0;
+      ++flying;
+      ++pu;
+    };
+#pragma unroll 1
+    for (int i = 0; i < STAGES; ++i) produce();
+
+    int stage = 0;
+    uint32_t phases = 0;
+    long long pos = u0;
+    bool dead = false;
+    // ---- items of the range
+    while (pos < u1) {
+      const int first = static_cast<int>(pos - base);
+      const long long item_end = base + w.seq.units;
+      const int last = static_cast<int>(min(static_cast<long long>(w.live), u1 - base));
+      const int row0 = w.rg * p.rows_per_item;
+      const int rows = min(p.rows_per_item, w.seq.qlen - row0);
+      const int see0 = w.seq.ctx - w.seq.qlen + row0 + 1;  // keys the item's first row sees
+      // q, scaled to fp16 by a power of two per column
+      uint32_t qf[2 * NC][NT][2];
+      float fac[NT][2];
+      int limB[NT], limA[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const bool on = rowB[nt] < rows;
+        const __nv_bfloat16* src =
+            p.q + (static_cast<long long>(w.seq.q0 + row0 + (on ? rowB[nt] : 0)) * p.num_q_heads + w.h * p.group +
+                   headB[nt]) * D;
+        uint32_t raw[2 * NC][2];
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2 * NC; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            raw[k][i] = on ? *reinterpret_cast<const uint32_t*>(src + k * 16 + i * 8 + 2 * qd) : 0u;
+            const uint32_t a = raw[k][i] & 0x7fff7fffu;
+            top = fmaxf(top, fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)));
+          }
+        top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // top in [2^e, 2^(e+1))
+        if (e < -126) e = top > 0.f ? -126 : 0;
+        if (e > 126) e = 126;
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int k = 0; k < 2 * NC; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qf[k][nt][i] = pack_f16x2(__uint_as_float(raw[k][i] << 16) * down,
+                                      __uint_as_float(raw[k][i] & 0xffff0000u) * down);
+        const float f = ldexpf(p.scale_log2, e);
+        fac[nt][0] = __shfl_sync(FULL_MASK, f, 8 * qd);  // column 2 qd lives in lanes 4 (2 qd) ..
+        fac[nt][1] = __shfl_sync(FULL_MASK, f, 8 * qd + 4);
+        limB[nt] = on ? see0 + rowB[nt] : 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) limA[nt][i] = rowA[nt][i] < rows ? see0 + rowA[nt][i] : 0;
+      }
+      // the constant part of each chunk's scores, -(264 or 24) times q summed
+      float cst[NC][NT][2];
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 2 * c; k < 2 * c + 2; ++k)
+            mma_f16_16816(d, 0xdc20dc20u, 0xdc20dc20u, 0xce00ce00u, 0xce00ce00u, qf[k][nt][0], qf[k][nt][1]);
+          cst[c][nt][0] = d[0];
+          cst[c][nt][1] = d[1];
+        }
+      float o[2 * NC][NT][4];
+      float l[NT][2], m[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 2 * NC; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[k][nt][i] = 0.f;
+        l[nt][0] = l[nt][1] = 0.f;
+        m[nt][0] = m[nt][1] = I4_NO_MAX;
+      }
+
+#pragma unroll 1
+      for (int u = first; u < last; ++u) {
+        const uint8_t* kb = ring + stage * C::STAGE_BYTES;
+        const unsigned lost = (bad >> (2 * stage)) & 3u;
+        if (!dead && !mbar_wait(bar + stage, (phases >> stage) & 1)) dead = true;
+        dead = __any_sync(FULL_MASK, dead);
+        if (dead) break;
+        phases ^= 1u << stage;
+        --flying;
+        const bool partial = u * I4_UNIT + I4_UNIT > see0 || lost;  // some key is masked for some column
+        const uint32_t ka = smem_u32(kb);
+
+        // ---- scores of 32 keys
+        float s[2][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t rb = ka + (bs == 16 ? mt * rec : mt * 16 * (D / 2));
+          const uint32_t sb = ka + (bs == 16 ? mt * rec + 16 * (D / 2) : 32 * (D / 2) + mt * 16 * (2 * NC));
+          uint32_t sc0[NC / 2], sc1[NC / 2];
+          lds_words(sb + g * 2 * NC, sc0);
+          lds_words(sb + (g + 8) * 2 * NC, sc1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.f;
+#pragma unroll
+          for (int cp = 0; cp < NC / 2; ++cp) {
+            uint32_t r[4];
+            ldsm_x4(rb + (code_at ^ (cp * 32)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // chunk 2 cp + x: rows 0-7 in r[2 x], rows 8-15 in r[2 x + 1]
+              const int c = 2 * cp + x;
+              uint32_t a[4], b[4];
+              i4_expand(r[2 * x], a);
+              i4_expand(r[2 * x + 1], b);
+              const float f0 = half_of(sc0[cp], x), f1 = half_of(sc1[cp], x);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float d[4] = {cst[c][nt][0], cst[c][nt][1], cst[c][nt][0], cst[c][nt][1]};
+                mma_f16_16816(d, a[0], b[0], a[1], b[1], qf[2 * c][nt][0], qf[2 * c][nt][1]);
+                mma_f16_16816(d, a[2], b[2], a[3], b[3], qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
+                s[mt][nt][0] = fmaf(d[0], f0, s[mt][nt][0]);
+                s[mt][nt][1] = fmaf(d[1], f0, s[mt][nt][1]);
+                s[mt][nt][2] = fmaf(d[2], f1, s[mt][nt][2]);
+                s[mt][nt][3] = fmaf(d[3], f1, s[mt][nt][3]);
+              }
+            }
+          }
+        }
+        // ---- softmax: y = score - m
+        const int key0 = u * I4_UNIT + g;
+        float top = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (partial) {
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt)
+                if (key0 + mt * 16 + (i >> 1) * 8 >= limA[nt][i & 1] || ((lost >> mt) & 1)) s[mt][nt][i] = -INFINITY;
+              // (a column whose scale factor is zero or negative must not turn -inf around)
+            }
+          }
+        float y[2][NT][4];
+        const auto relative = [&]() {
+          top = -1.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float x = fmaf(s[mt][nt][i], fac[nt][i & 1], -m[nt][i & 1]);
+                if (partial && s[mt][nt][i] == -INFINITY) x = -INFINITY;
+                y[mt][nt][i] = x;
+                top = fmaxf(top, x);
+              }
+        };
+        relative();
+        if (__any_sync(FULL_MASK, top > 0.f)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float mx = -INFINITY;
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int i = j; i < 4; i += 2)
+                  if (!(partial && s[mt][nt][i] == -INFINITY)) mx = fmaxf(mx, s[mt][nt][i] * fac[nt][j]);
+              mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 16));
+              const float mn = mx > m[nt][j] ? mx + 1.f : m[nt][j];
+              const float a = fast_exp2(m[nt][j] - mn);
+              m[nt][j] = mn;
+              l[nt][j] *= a;
+#pragma unroll
+              for (int k = 0; k < 2 * NC; ++k) {
+                o[k][nt][j] *= a;
+                o[k][nt][j + 2] *= a;
+              }
+            }
+          relative();
+        }
+        uint32_t pf[2][NT][2];  // B operand: keys 2 qd, 2 qd + 1 (and + 8) of column g
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[i] = fast_exp2(y[mt][nt][i]);
+              l[nt][i & 1] += e[i];
+            }
+            pf[mt][nt][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
+            pf[mt][nt][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
+          }
+        // ---- values
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t va = ka + C::HALF_BYTES;
+          const uint32_t rb = va + (bs == 16 ? mt * rec : mt * 16 * (D / 2));
+          const uint32_t sb = va + (bs == 16 ? mt * rec + 16 * (D / 2) : 32 * (D / 2) + mt * 16 * (2 * NC));
+          uint32_t w0[NC / 2], w1[NC / 2], w2[NC / 2], w3[NC / 2];
+          lds_words(sb + (2 * qd) * 2 * NC, w0);
+          lds_words(sb + (2 * qd + 1) * 2 * NC, w1);
+          lds_words(sb + (2 * qd + 8) * 2 * NC, w2);
+          lds_words(sb + (2 * qd + 9) * 2 * NC, w3);
+#pragma unroll
+          for (int cp = 0; cp < NC / 2; ++cp) {
+            uint32_t r[4];
+            ldsm_x4_trans(rb + (code_at ^ (cp * 32)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // chunk 2 cp + x: keys 0-7 in r[2 x], keys 8-15 in r[2 x + 1]
+              const int c = 2 * cp + x;
+              uint32_t a[4], b[4];
+              i4_expand(r[2 * x], a);
+              i4_expand(r[2 * x + 1], b);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t off = i & 1 ? 0x4e004e00u : 0x5c205c20u;  // 24, 264
+                a[i] = hsub2(a[i], off);
+                b[i] = hsub2(b[i], off);
+              }
+              const uint32_t s01 = __byte_perm(w0[cp], w1[cp], x ? 0x7632 : 0x5410);
+              const uint32_t s89 = __byte_perm(w2[cp], w3[cp], x ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                uint32_t b0 = hmul2(pf[mt][nt][0], s01), b1 = hmul2(pf[mt][nt][1], s89);
+                if (partial) {  // a masked key's scale may be anything: its weight is zero, not zero times that
+                  const int k0 = u * I4_UNIT + mt * 16 + 2 * qd;
+                  const int lim = (lost >> mt) & 1 ? 0 : limB[nt];
+                  b0 &= (k0 < lim ? 0xffffu : 0u) | (k0 + 1 < lim ? 0xffff0000u : 0u);
+                  b1 &= (k0 + 8 < lim ? 0xffffu : 0u) | (k0 + 9 < lim ? 0xffff0000u : 0u);
+                }
+                mma_f16_16816(o[2 * c][nt], a[0], a[1], b[0], b[1], b0, b1);
+                mma_f16_16816(o[2 * c + 1][nt], a[2], a[3], b[2], b[3], b0, b1);
+              }
+            }
+          }
+        }
+        __syncwarp();  // every lane has read the stage
+        if (++stage == STAGES) stage = 0;
+        produce();
+      }
+      // ---- the item's end, or the range's
+      const bool starts = pos == base, finishes = item_end <= u1;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 4; x <= 16; x <<= 1) l[nt][j] += __shfl_xor_sync(FULL_MASK, l[nt][j], x);
+      if (starts && finishes) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
+          __nv_bfloat16* dst =
+              p.out + (static_cast<long long>(w.seq.q0 + row0 + rowB[nt]) * p.num_q_heads + w.h * p.group +
+                       headB[nt]) * D + 2 * qd;
+#pragma unroll
+          for (int k = 0; k < 2 * NC; ++k) {
+            const uint32_t a = movmatrix_trans(pack_bf16x2(o[k][nt][0] * i0, o[k][nt][1] * i1));
+            const uint32_t b = movmatrix_trans(pack_bf16x2(o[k][nt][2] * i0, o[k][nt][3] * i1));
+            if (rowB[nt] < rows) {
+              *reinterpret_cast<uint32_t*>(dst + k * 16) = a;
+              *reinterpret_cast<uint32_t*>(dst + k * 16 + 8) = b;
+            }
+          }
+        }
+      } else {
+        const int slot = starts ? 1 : 0;
+        float* rec_out = piece0 + slot * C::PIECE;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int col = nt * 8 + 2 * qd + j;
+#pragma unroll
+            for (int k = 0; k < 2 * NC; ++k) {
+              rec_out[col * D + k * 16 + g] = o[k][nt][j];
+              rec_out[col * D + k * 16 + 8 + g] = o[k][nt][j + 2];
+            }
+            if (g == 0) {
+              rec_out[COLS * D + col] = m[nt][j];
+              rec_out[COLS * (D + 1) + col] = l[nt][j];
+            }
+          }
+        end.row[slot] = w.seq.q0 + row0;
+        end.rows[slot] = rows;
+        end.h[slot] = w.h;
+        end.first[slot] = base;
+        end.units[slot] = w.seq.units;
+        if (slot == 0) {
+          end.has0 = 1;
+          end.on0 = !finishes;
+        } else {
+          end.has1 = 1;
+        }
+      }
+      pos = min(item_end, u1);
+      if (pos < u1) {
+        base = item_end;
+        i4_next(p, w);
+      }
+    }
+    if (dead) {  // a copy did not land in time: report it, and give those in flight as long again
+      if (lane == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_TIMEOUT));
+      for (; flying > 0; --flying) {
+        (void)mbar_wait(bar + stage, (phases >> stage) & 1);
+        if (++stage == STAGES) stage = 0;
+      }
+    }
+  }
+  if (lane == 0) ends[warp] = end;
+  __syncthreads();
+
+  // ---- merge the CTA's pieces.  Chain e: the item the CTA's range starts inside
+  // of (e = 0), or the one that starts in warp e - 1 and goes on past it.
+  float* cta_piece = p.cta_pieces + static_cast<long long>(blockIdx.x) * 2 * C::PIECE;
+  const float* pieces = p.warp_pieces + static_cast<long long>(blockIdx.x) * WARPS * 2 * C::PIECE;
+  int job = 0;
+  for (int e = 0; e <= WARPS; ++e) {
+    if (e == 0 ? !ends[0].has0 : !ends[e - 1].has1) continue;
+    const int w0 = e == 0 ? 0 : e - 1, sl = e == 0 ? 0 : 1;
+    int w1 = e == 0 ? (ends[0].on0 ? 1 : 0) : e;  // last warp of the chain
+    if (e > 0 || ends[0].on0) {
+      while (w1 < WARPS - 1 && (!ends[w1].has0 || ends[w1].on0)) ++w1;
+    }
+    if (w1 > WARPS - 1) w1 = WARPS - 1;
+    const WarpEnd& we = ends[w0];
+    const long long first = we.first[sl], after = first + we.units[sl];
+    const bool inside = first >= c0 && after <= c0 + cn;
+    const int cols = we.rows[sl] * p.group;
+    const auto piece = [&](int k) -> const float* {
+      if (k > 0 && !ends[w0 + k].has0) return nullptr;  // a warp without units
+      return pieces + (static_cast<long long>(w0 + k) * 2 + (k == 0 ? sl : 0)) * C::PIECE;
+    };
+    const int n = w1 - w0 + 1;
+    for (int col = 0; col < cols; ++col, ++job) {
+      if (job % WARPS != warp) continue;
+      const int r = col / p.group, hh = col - r * p.group;
+      __nv_bfloat16* out =
+          p.out + (static_cast<long long>(we.row[sl] + r) * p.num_q_heads + we.h[sl] * p.group + hh) * D;
+      merge_column<D, COLS>(piece, n, col, lane, inside ? out : nullptr, cta_piece + (e == 0 ? 0 : 1) * C::PIECE);
+    }
+  }
+  // ---- pieces of items that cross CTAs: count them in; the last CTA merges
+  __threadfence();
+  __syncthreads();
+  for (int e = 0; e <= 1; ++e) {  // 0: the item this range starts inside of; 1: the one that goes on past it
+    int src = -1;
+    if (e == 0) {
+      if (ends[0].has0) src = 0;
+    } else {
+      for (int w = 0; w < WARPS; ++w)
+        if (ends[w].has1) src = w;
+    }
+    if (src < 0) continue;
+    const WarpEnd& we = ends[src];
+    const long long first = we.first[e], after = first + we.units[e];
+    if (e == 1 && after <= c0 + cn) continue;  // merged above
+    const int f = cta_of(first), t = cta_of(after - 1);
+    const int n = t - f + 1;
+    if (tid == 0) {
+      const int got = atomicAdd(p.counters + f, 1);
+      sh_merge = got == n - 1;
+      if (got == n - 1) p.counters[f] = 0;
+      __threadfence();
+    }
+    __syncthreads();
+    if (sh_merge) {
+      const int cols = we.rows[e] * p.group;
+      const auto piece = [&](int k) -> const float* {  // the first CTA's piece starts in it (slot 1), the others' came from before (slot 0)
+        return p.cta_pieces + (static_cast<long long>(f + k) * 2 + (k == 0 ? 1 : 0)) * C::PIECE;
+      };
+      for (int col = warp; col < cols; col += WARPS) {
+        const int r = col / p.group, hh = col - r * p.group;
+        merge_column<D, COLS>(
+            piece, n, col, lane,
+            p.out + (static_cast<long long>(we.row[e] + r) * p.num_q_heads + we.h[e] * p.group + hh) * D, nullptr);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+constexpr size_t I4_COUNTER_BYTES = 4096;  // one int per CTA
+
+template <int D, int NT>
+size_t workspace_of(int num_sms) {
+  using C = I4<D, NT>;
+  return I4_COUNTER_BYTES + sizeof(float) * static_cast<size_t>(num_sms) * 2 * C::PIECE * (C::WARPS + 1);
+}
+
+size_t int4_workspace(int head_dim, int num_sms) {
+  size_t n = 0;
+  const auto most = [&](size_t x) { n = x > n ? x : n; };
+  if (head_dim == 64) most(workspace_of<64, 1>(num_sms)), most(workspace_of<64, 2>(num_sms));
+  if (head_dim == 128) most(workspace_of<128, 1>(num_sms)), most(workspace_of<128, 2>(num_sms));
+  if (head_dim == 256) most(workspace_of<256, 1>(num_sms));
+  return (n + 255) / 256 * 256;
+}
+
+template <int D, int NT>
+int launch_int4(Int4Params& p, void* workspace, cudaStream_t stream, int num_sms) {
+  using C = I4<D, NT>;
+  p.rows_per_item = p.query_start ? C::COLS / p.group : 1;
+  p.counters = static_cast<int*>(workspace);
+  p.warp_pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + I4_COUNTER_BYTES);
+  p.cta_pieces = p.warp_pieces + static_cast<size_t>(num_sms) * 2 * C::PIECE * C::WARPS;
+  static PerDevice ready;
+  int done = 0;
+  const int rc = per_device(
+      ready,
+      [](int) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(int4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        return e == cudaSuccess ? 1 : cuda_fail(e, "cudaFuncSetAttribute");
+      },
+      &done);
+  if (rc != PA_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return check_launch(cudaLaunchKernelEx(&cfg, int4_kernel<D, NT>, p), "int4_kernel launch");
 }
 
 int run_int4(void* out, const void* q, const int32_t* query_start, const void* k_cache, const void* v_cache,
@@ -116,7 +879,7 @@ int run_int4(void* out, const void* q, const int32_t* query_start, const void* k
   const int group = num_q_heads / num_kv_heads;
   if (block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
   if (!rows_supported(group, head_dim)) return PA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(max_blocks) * block_size > INT32_MAX) return PA_ERR_SHAPE;
+  if (static_cast<long long>(max_blocks) * block_size > INT32_MAX - I4_UNIT) return PA_ERR_SHAPE;
   if (num_seqs == 0 || total_rows == 0) return PA_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !workspace) return PA_ERR_NULL;
   const auto ok = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
@@ -124,17 +887,35 @@ int run_int4(void* out, const void* q, const int32_t* query_start, const void* k
   DeviceInfo di;
   const int rc = device_info(&di);
   if (rc != PA_OK) return rc;
-  if (workspace_bytes < pa_int4_workspace_bytes(num_q_heads, num_kv_heads, head_dim)) return PA_ERR_WORKSPACE;
-  Int4Params p{static_cast<__nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(q),
-               static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), block_tables, context_lens,
-               query_start, num_seqs, total_rows, max_blocks, num_q_heads, num_kv_heads, group,
-               block_size == 16 ? 4 : 5, num_blocks, scale * 1.4426950408889634f, dev_status};
-  const dim3 grid(total_rows, num_q_heads);
+  if (di.num_sms * static_cast<int>(sizeof(int)) > static_cast<int>(I4_COUNTER_BYTES)) return PA_ERR_UNSUPPORTED;
+  if (workspace_bytes < int4_workspace(head_dim, di.num_sms)) return PA_ERR_WORKSPACE;
+  Int4Params p{};
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.query_start = query_start;
+  p.num_seqs = num_seqs;
+  p.num_rows = total_rows;
+  p.max_blocks = max_blocks;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = group;
+  p.block_shift = block_size == 16 ? 4 : 5;
+  p.num_blocks = num_blocks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.status = dev_status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (head_dim == 64) int4_simple_kernel<64><<<grid, 32 * I4_WARPS, 0, st>>>(p);
-  else if (head_dim == 128) int4_simple_kernel<128><<<grid, 32 * I4_WARPS, 0, st>>>(p);
-  else int4_simple_kernel<256><<<grid, 32 * I4_WARPS, 0, st>>>(p);
-  return check_launch(cudaSuccess, "int4_simple_kernel launch");
+  // One n-tile of columns where 8 hold a row's heads and the call has one row per sequence; two for wider groups,
+  // and for several rows, which then share each unpacked key.
+  const bool two = group > 8 || query_start;
+  if (head_dim == 64)
+    return two ? launch_int4<64, 2>(p, workspace, st, di.num_sms) : launch_int4<64, 1>(p, workspace, st, di.num_sms);
+  if (head_dim == 128)
+    return two ? launch_int4<128, 2>(p, workspace, st, di.num_sms) : launch_int4<128, 1>(p, workspace, st, di.num_sms);
+  return launch_int4<256, 1>(p, workspace, st, di.num_sms);
 }
 
 }  // namespace
@@ -146,7 +927,9 @@ extern "C" {
 size_t pa_int4_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim) {
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads) return 0;
   if (!pa::rows_supported(num_q_heads / num_kv_heads, head_dim)) return 0;
-  return 256;
+  pa::DeviceInfo di;
+  if (pa::device_info(&di) != PA_OK) return 0;
+  return pa::int4_workspace(head_dim, di.num_sms);
 }
 
 int pa_decode_int4(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,

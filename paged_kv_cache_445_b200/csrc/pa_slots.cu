@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) slots_kernel(const SlotsParams p
     p.slots[t] = -1;
   }
   // every CTA has read the lengths and the queue state: now they may change
+  __threadfence();
   cg::this_cluster().sync();
   if (rank != 0) return;
   const int taken = sh.taken;
@@ -274,6 +275,8 @@ __global__ void __launch_bounds__(SLOT_THREADS) slots_kernel(const SlotsParams p
       p.free_state_out[1] = p.free_state[1];
     }
   }
+  // An attention kernel launched behind this one reads the lengths in its prologue, once every CTA here has ended.
+  __threadfence();
 }
 
 }  // namespace

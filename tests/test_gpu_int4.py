@@ -134,11 +134,15 @@ def test_many_sequences():
     b.check()
 
 
-def test_rows_equal_decode_and_repeat_bit_for_bit():
-    b = Batch([500, 33, 1200], [1, 1, 1], 16, 2, 128, 16, seed=3)
-    assert b.run() == 0
+@pytest.mark.parametrize("varlen", [False, True])
+def test_repeats_bit_for_bit(varlen):
+    """Pieces are merged in their order whoever brings the last one (the two entry points cut the keys at different
+    places, so they agree up to rounding only)."""
+    b = Batch([500, 33, 20000], [1, 1, 1], 16, 2, 128, 16, seed=3)
+    assert b.run(varlen) == 0
+    b.check()
     first = b.out.clone()
-    for varlen in (False, True, True):
+    for _ in range(5):
         out = torch.zeros_like(b.out)
         assert b.run(varlen, out) == 0
         assert torch.equal(out, first)
