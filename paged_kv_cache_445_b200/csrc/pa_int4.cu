@@ -43,8 +43,8 @@ namespace pa {
 namespace {
 
 constexpr int I4_UNIT = 32;        // keys
-constexpr int I4_BUCKETS = 1024;   // prefix sums of the batch's units, of runs of sequences
-constexpr float I4_NO_MAX = -3e38f;
+constexpr int I4_BUCKETS = 512;    // prefix sums of the batch's units, of runs of sequences
+constexpr float I4_NO_MAX = -3e38f; // maximum over no pieces
 
 template <int D, int NT>
 struct I4 {
@@ -139,22 +139,23 @@ __device__ __forceinline__ void i4_next(const Int4Params& p, Walk& w) {
   }
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
-// 8 codes (nibbles of the two halves of w) -> 4 fp16 pairs: 256 + u in 0 and 2, 16 + u in 1 and 3.
+// 8 codes (nibbles of the two halves of w) -> 4 fp16 pairs: 1024 + u in 0 and 2, 64 + u in 1 and 3 (the nibble
+// lies in the mantissa where its lowest bit is worth one: five operations).
 __device__ __forceinline__ void i4_expand(uint32_t w, uint32_t (&h)[4]) {
-  const uint32_t a = w << 2, b = w >> 6;
-  h[0] = (a & 0x003c003cu) | 0x5c005c00u;
-  h[1] = (a & 0x03c003c0u) | 0x4c004c00u;
-  h[2] = (b & 0x003c003cu) | 0x5c005c00u;
-  h[3] = (b & 0x03c003c0u) | 0x4c004c00u;
+  const uint32_t b = w >> 8;
+  h[0] = (w & 0x000f000fu) | 0x64006400u;
+  h[1] = (w & 0x00f000f0u) | 0x54005400u;
+  h[2] = (b & 0x000f000fu) | 0x64006400u;
+  h[3] = (b & 0x00f000f0u) | 0x54005400u;
 }
+constexpr uint32_t I4_OFF_EVEN = 0x64086408u, I4_OFF_ODD = 0x54805480u;    // 1024 + 8, 64 + 8
+constexpr uint32_t I4_NEG_EVEN = 0xe408e408u, I4_NEG_ODD = 0xd480d480u;
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -253,7 +254,14 @@ struct WarpEnd {
   int units[2];
 };
 
-template <int D, int NT>
+// State of a warp's walk over its items that only item changes touch.
+struct WarpState {
+  Walk c, p;               // consumer's and producer's place
+  long long cbase, pbase;  // first units of their items
+};
+
+// VARLEN: several query rows per sequence (columns see different numbers of keys).
+template <int D, int NT, bool VARLEN>
 __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __grid_constant__ Int4Params p) {
   using C = I4<D, NT>;
   constexpr int NC = C::NC, COLS = C::COLS, WARPS = C::WARPS, STAGES = C::STAGES;
@@ -262,12 +270,14 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES + 8 * I4_BUCKETS);
   __shared__ long long scan[WARPS];
   __shared__ WarpEnd ends[WARPS];
+  __shared__ WarpState walks[WARPS];
   __shared__ int sh_merge;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, qd = lane & 3;
   const int bs = 1 << p.block_shift;
 
   if (lane == 0) {
+    ends[warp].has0 = ends[warp].on0 = ends[warp].has1 = 0;
     for (int i = 0; i < STAGES; ++i) mbar_init(&bars[warp * STAGES + i], 1);
     fence_mbar_init();
   }
@@ -332,30 +342,23 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   const long long u0 = c0 + (warp * cn + WARPS - 1) / WARPS, u1 = c0 + ((warp + 1) * cn + WARPS - 1) / WARPS;
   float* piece0 = p.warp_pieces + (static_cast<long long>(blockIdx.x) * WARPS + warp) * 2 * C::PIECE;
 
-  // column constants: column g + 8 nt of the B operand, columns 2 qd and 2 qd + 1 of the accumulators
-  int rowB[NT], headB[NT], rowA[NT][2];
+  // column constants: rows of column g + 8 nt of the B operand and of columns 2 qd, 2 qd + 1 of the accumulators
+  int colrow[NT];  // three bytes
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int c = nt * 8 + g;
-    rowB[nt] = c / p.group;
-    headB[nt] = c - rowB[nt] * p.group;
-    rowA[nt][0] = (nt * 8 + 2 * qd) / p.group;
-    rowA[nt][1] = (nt * 8 + 2 * qd + 1) / p.group;
-  }
+  for (int nt = 0; nt < NT; ++nt)
+    colrow[nt] = (nt * 8 + g) / p.group | (nt * 8 + 2 * qd) / p.group << 8 | (nt * 8 + 2 * qd + 1) / p.group << 16;
+  const auto rowB = [&](int nt) { return colrow[nt] & 0xff; };
+  const auto rowA = [&](int nt, int j) { return colrow[nt] >> (8 + 8 * j) & 0xff; };
   // ldmatrix: lane i gives row (i & 7) + 8 ((i >> 3) & 1) of chunk i >> 4 (+ 2 per step)
-  const int lrow = (lane & 7) + (lane & 8);
-  const uint32_t code_at = int4_code_offset<D>(lrow, lane >> 4);
+  const uint32_t code_at = int4_code_offset<D>((lane & 7) + (lane & 8), lane >> 4);
   uint8_t* ring = smem + warp * STAGES * C::STAGE_BYTES;
   uint64_t* bar = bars + warp * STAGES;
-  const uint64_t policy = policy_evict_first();
   const int rec = int4_record_bytes(bs, D);
-  const int blocks_per_unit = I4_UNIT >> p.block_shift;  // 2 or 1
+  const int unit_shift = 5 - p.block_shift;  // log2 of the blocks of a unit
+  WarpState& ws = walks[warp];
 
-  WarpEnd end{};
   if (u0 < u1) {
     // ---- find the item of u0
-    Walk w;
-    long long base;  // first unit of the item
     {
       int lo = 0, hi = I4_BUCKETS - 1;
       while (lo < hi) {
@@ -363,6 +366,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         if (prefix[mid] > u0) hi = mid; else lo = mid + 1;
       }
       long long at = lo > 0 ? prefix[lo - 1] : 0;
+      Walk w;
       int s = lo * run;
       for (;; ++s) {
         w.seq = i4_seq(p, s);
@@ -375,73 +379,81 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       w.s = s;
       w.rg = static_cast<int>(item / p.num_kv_heads);
       w.h = static_cast<int>(item - static_cast<long long>(w.rg) * p.num_kv_heads);
-      base = at + item * w.seq.units;
       i4_enter(p, w);
+      if (lane == 0) {
+        ws.c = ws.p = w;
+        ws.cbase = ws.pbase = at + item * w.seq.units;
+      }
+      __syncwarp();
     }
     // ---- producer: the same walk, ahead by up to STAGES units
-    Walk pw = w;
-    long long pbase = base;
-    int pu = static_cast<int>(u0 - base);
-    int pend = static_cast<int>(min(static_cast<long long>(w.live), u1 - base));
+    int pu = static_cast<int>(u0 - ws.pbase), pend = static_cast<int>(min(static_cast<long long>(ws.p.live), u1 - ws.pbase));
+    int entries = (ws.p.seq.ctx + bs - 1) >> p.block_shift, head_off = ws.p.h * rec;
     int ids = 0, ids_from = INT32_MAX;  // block IDs of 32 table entries from ids_from on, one per lane
-    int pstage = 0, flying = 0;  // flying: units loaded and not yet waited for
-    unsigned bad = 0;  // two bits per stage: blocks of its unit that were not loaded
+    int flying = 0;                     // units loaded and not yet waited for
+    unsigned bad = 0;                   // two bits per stage: blocks of its unit that were not loaded
+    // lanes 0 .. 3 copy K and V (lane & 1) of the unit's first and second block (lane >> 1)
+    const uint8_t* cache = (lane & 1 ? p.v_cache : p.k_cache);
+    const uint32_t copy_to = smem_u32(ring) + (lane & 1) * C::HALF_BYTES + (lane >> 1 & 1) * rec;
 
-    const auto produce = [&]() {
-      while (pu >= pend) {
-        if (pbase + pw.seq.units >= u1) return;
-        pbase += pw.seq.units;
-        i4_next(p, pw);
-        pu = 0;
-        pend = static_cast<int>(min(static_cast<long long>(pw.live), u1 - pbase));
+    const auto produce = [&](int to) {
+      if (pu >= pend) {
+        do {
+          const long long next = ws.pbase + ws.p.seq.units;
+          if (next >= u1) {
+            pend = 0;
+            return;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            ws.pbase = next;
+            i4_next(p, ws.p);
+          }
+          __syncwarp();
+          pu = 0;
+          pend = static_cast<int>(min(static_cast<long long>(ws.p.live), u1 - next));
+        } while (pend <= 0);
+        entries = (ws.p.seq.ctx + bs - 1) >> p.block_shift;
+        head_off = ws.p.h * rec;
         ids_from = INT32_MAX;
       }
-      const int entry = pu * blocks_per_unit;
-      const int entries = (pw.seq.ctx + bs - 1) >> p.block_shift;
-      if (entry < ids_from || entry + blocks_per_unit > ids_from + 32) {
+      const int entry = pu << unit_shift;
+      if (entry < ids_from || entry >= ids_from + 32) {
         ids_from = entry;
         ids = entry + lane < entries
-                  ? __ldg(p.block_tables + static_cast<long long>(pw.s) * p.max_blocks + entry + lane)
+                  ? __ldg(p.block_tables + static_cast<long long>(ws.p.s) * p.max_blocks + entry + lane)
                   : -1;
       }
-      const int id0 = __shfl_sync(FULL_MASK, ids, entry - ids_from);
-      const int id1 = blocks_per_unit == 2 ? __shfl_sync(FULL_MASK, ids, entry + 1 - ids_from) : 0;
-      const bool in1 = blocks_per_unit == 2 && entry + 1 < entries;
-      const bool ok0 = id0 >= 0 && id0 < p.num_blocks, ok1 = in1 && id1 >= 0 && id1 < p.num_blocks;
-      unsigned b = 0;
-      if (!ok0 || (in1 && !ok1)) {
-        b = blocks_per_unit == 1 ? 3u : (ok0 ? 0u : 1u) | (in1 && !ok1 ? 2u : 0u);
+      const int mine = entry + (lane >> 1 & unit_shift);  // (unit_shift is 1 or 0: the second block, or the first again)
+      const int id = __shfl_sync(FULL_MASK, ids, mine - ids_from);
+      const bool in = lane < 2 << unit_shift && mine < entries;
+      const bool ok = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
+      const unsigned go = __ballot_sync(FULL_MASK, in && ok);
+      const unsigned lost = __ballot_sync(FULL_MASK, in && !ok);
+      bad &= ~(3u << (2 * to));
+      if (lost) {
+        bad |= (unit_shift ? (lost & 1) | (lost >> 1 & 2) : 3u) << (2 * to);
         if (lane == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
       }
-      bad = (bad & ~(3u << (2 * pstage))) | (b << (2 * pstage));
-      if (lane == 0) {
-        uint8_t* dst = ring + pstage * C::STAGE_BYTES;
-        uint64_t* fb = bar + pstage;
-        mbar_arrive_expect_tx(fb, 2 * rec * ((ok0 ? 1 : 0) + (ok1 ? 1 : 0)));
-        if (ok0) {
-          const long long at = (static_cast<long long>(id0) * p.num_kv_heads + pw.h) * rec;
-          bulk_load(dst, p.k_cache + at, rec, fb, policy);
-          bulk_load(dst + C::HALF_BYTES, p.v_cache + at, rec, fb, policy);
-        }
-        if (ok1) {
-          const long long at = (static_cast<long long>(id1) * p.num_kv_heads + pw.h) * rec;
-          bulk_load(dst + rec, p.k_cache + at, rec, fb, policy);
-          bulk_load(dst + C::HALF_BYTES + rec, p.v_cache + at, rec, fb, policy);
-        }
-      }
-      if (++pstage == STAGES) pstage = 0;
+      if (lane == 0) mbar_arrive_expect_tx(bar + to, __popc(go) * rec);
+      __syncwarp();
+      if (in && ok)
+        bulk_load(copy_to + to * C::STAGE_BYTES, cache + static_cast<long long>(id) * p.num_kv_heads * rec + head_off, rec,
+                  bar + to);
       ++flying;
       ++pu;
     };
 #pragma unroll 1
-    for (int i = 0; i < STAGES; ++i) produce();
+    for (int i = 0; i < STAGES; ++i) produce(i);
 
     int stage = 0;
-    uint32_t phases = 0;
+    uint32_t phase = 0;
     long long pos = u0;
     bool dead = false;
     // ---- items of the range
     while (pos < u1) {
+      const Walk w = ws.c;
+      const long long base = ws.cbase;
       const int first = static_cast<int>(pos - base);
       const long long item_end = base + w.seq.units;
       const int last = static_cast<int>(min(static_cast<long long>(w.live), u1 - base));
@@ -451,20 +463,19 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       // q, scaled to fp16 by a power of two per column
       uint32_t qf[2 * NC][NT][2];
       float fac[NT][2];
-      int limB[NT], limA[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const bool on = rowB[nt] < rows;
+        const bool on = rowB(nt) < rows;
+        const int row = on ? rowB(nt) : 0, head = nt * 8 + g - row * p.group;
         const __nv_bfloat16* src =
-            p.q + (static_cast<long long>(w.seq.q0 + row0 + (on ? rowB[nt] : 0)) * p.num_q_heads + w.h * p.group +
-                   headB[nt]) * D;
+            p.q + (static_cast<long long>(w.seq.q0 + row0 + row) * p.num_q_heads + w.h * p.group + head) * D + 2 * qd;
         uint32_t raw[2 * NC][2];
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < 2 * NC; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            raw[k][i] = on ? *reinterpret_cast<const uint32_t*>(src + k * 16 + i * 8 + 2 * qd) : 0u;
+            raw[k][i] = on ? *reinterpret_cast<const uint32_t*>(src + k * 16 + i * 8) : 0u;
             const uint32_t a = raw[k][i] & 0x7fff7fffu;
             top = fmaxf(top, fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)));
           }
@@ -483,11 +494,8 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         const float f = ldexpf(p.scale_log2, e);
         fac[nt][0] = __shfl_sync(FULL_MASK, f, 8 * qd);  // column 2 qd lives in lanes 4 (2 qd) ..
         fac[nt][1] = __shfl_sync(FULL_MASK, f, 8 * qd + 4);
-        limB[nt] = on ? see0 + rowB[nt] : 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) limA[nt][i] = rowA[nt][i] < rows ? see0 + rowA[nt][i] : 0;
       }
-      // the constant part of each chunk's scores, -(264 or 24) times q summed
+      // the constant part of each chunk's scores: -1032 or -72 times q, summed
       float cst[NC][NT][2];
 #pragma unroll
       for (int c = 0; c < NC; ++c)
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 2 * c; k < 2 * c + 2; ++k)
-            mma_f16_16816(d, 0xdc20dc20u, 0xdc20dc20u, 0xce00ce00u, 0xce00ce00u, qf[k][nt][0], qf[k][nt][1]);
+            mma_f16_16816(d, I4_NEG_EVEN, I4_NEG_EVEN, I4_NEG_ODD, I4_NEG_ODD, qf[k][nt][0], qf[k][nt][1]);
           cst[c][nt][0] = d[0];
           cst[c][nt][1] = d[1];
         }
@@ -509,23 +517,23 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[k][nt][i] = 0.f;
         l[nt][0] = l[nt][1] = 0.f;
-        m[nt][0] = m[nt][1] = I4_NO_MAX;
+        m[nt][0] = m[nt][1] = 0.f;
       }
+      unsigned fresh = (1u << 2 * NT) - 1;  // columns without a score so far: their reference is not one yet
 
 #pragma unroll 1
       for (int u = first; u < last; ++u) {
-        const uint8_t* kb = ring + stage * C::STAGE_BYTES;
+        const uint32_t ka = smem_u32(ring) + stage * C::STAGE_BYTES;
         const unsigned lost = (bad >> (2 * stage)) & 3u;
-        if (!dead && !mbar_wait(bar + stage, (phases >> stage) & 1)) dead = true;
-        dead = __any_sync(FULL_MASK, dead);
-        if (dead) break;
-        phases ^= 1u << stage;
+        if (!__all_sync(FULL_MASK, !dead && mbar_wait(bar + stage, phase))) {
+          dead = true;
+          break;
+        }
         --flying;
         const bool partial = u * I4_UNIT + I4_UNIT > see0 || lost;  // some key is masked for some column
-        const uint32_t ka = smem_u32(kb);
 
         // ---- scores of 32 keys
-        float s[2][NT][4];
+        float y[2][NT][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           const uint32_t rb = ka + (bs == 16 ? mt * rec : mt * 16 * (D / 2));
@@ -536,7 +544,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.f;
+            for (int i = 0; i < 4; ++i) y[mt][nt][i] = 0.f;
 #pragma unroll
           for (int cp = 0; cp < NC / 2; ++cp) {
             uint32_t r[4];
@@ -553,69 +561,64 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
                 float d[4] = {cst[c][nt][0], cst[c][nt][1], cst[c][nt][0], cst[c][nt][1]};
                 mma_f16_16816(d, a[0], b[0], a[1], b[1], qf[2 * c][nt][0], qf[2 * c][nt][1]);
                 mma_f16_16816(d, a[2], b[2], a[3], b[3], qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
-                s[mt][nt][0] = fmaf(d[0], f0, s[mt][nt][0]);
-                s[mt][nt][1] = fmaf(d[1], f0, s[mt][nt][1]);
-                s[mt][nt][2] = fmaf(d[2], f1, s[mt][nt][2]);
-                s[mt][nt][3] = fmaf(d[3], f1, s[mt][nt][3]);
+                y[mt][nt][0] = fmaf(d[0], f0, y[mt][nt][0]);
+                y[mt][nt][1] = fmaf(d[1], f0, y[mt][nt][1]);
+                y[mt][nt][2] = fmaf(d[2], f1, y[mt][nt][2]);
+                y[mt][nt][3] = fmaf(d[3], f1, y[mt][nt][3]);
               }
             }
           }
         }
         // ---- softmax: y = score - m
-        const int key0 = u * I4_UNIT + g;
-        float top = 0.f;
+        float top = -1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (partial) {
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-              for (int mt = 0; mt < 2; ++mt)
-                if (key0 + mt * 16 + (i >> 1) * 8 >= limA[nt][i & 1] || ((lost >> mt) & 1)) s[mt][nt][i] = -INFINITY;
-              // (a column whose scale factor is zero or negative must not turn -inf around)
+            for (int i = 0; i < 4; ++i) {
+              y[mt][nt][i] = fmaf(y[mt][nt][i], fac[nt][i & 1], -m[nt][i & 1]);
+              if (!partial) top = fmaxf(top, y[mt][nt][i]);
             }
-          }
-        float y[2][NT][4];
-        const auto relative = [&]() {
-          top = -1.f;
+        if (partial) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                float x = fmaf(s[mt][nt][i], fac[nt][i & 1], -m[nt][i & 1]);
-                if (partial && s[mt][nt][i] == -INFINITY) x = -INFINITY;
-                y[mt][nt][i] = x;
-                top = fmaxf(top, x);
+                const int row = rowA(nt, i & 1);
+                if (u * I4_UNIT + mt * 16 + (i >> 1) * 8 + g >= (row < rows ? see0 + row : 0) || (lost >> mt & 1))
+                  y[mt][nt][i] = -INFINITY;
+                top = fmaxf(top, y[mt][nt][i]);
               }
-        };
-        relative();
-        if (__any_sync(FULL_MASK, top > 0.f)) {
+        }
+        if (__any_sync(FULL_MASK, top > 0.f || fresh)) {  // a score passes the reference: move it
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float mx = -INFINITY;
-#pragma unroll
-              for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int i = j; i < 4; i += 2)
-                  if (!(partial && s[mt][nt][i] == -INFINITY)) mx = fmaxf(mx, s[mt][nt][i] * fac[nt][j]);
+              float mx = fmaxf(fmaxf(y[0][nt][j], y[0][nt][j + 2]), fmaxf(y[1][nt][j], y[1][nt][j + 2]));
               mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 16));
-              const float mn = mx > m[nt][j] ? mx + 1.f : m[nt][j];
-              const float a = fast_exp2(m[nt][j] - mn);
-              m[nt][j] = mn;
+              const bool first_one = fresh >> (2 * nt + j) & 1;
+              const float up = mx > 0.f || (first_one && mx > -INFINITY) ? mx + 1.f : 0.f;
+              const float a = first_one ? 0.f : fast_exp2(-up);
+              if (mx > -INFINITY) fresh &= ~(1u << (2 * nt + j));
+              m[nt][j] = m[nt][j] + up;
               l[nt][j] *= a;
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                y[mt][nt][j] -= up;
+                y[mt][nt][j + 2] -= up;
+              }
 #pragma unroll
               for (int k = 0; k < 2 * NC; ++k) {
                 o[k][nt][j] *= a;
                 o[k][nt][j + 2] *= a;
               }
             }
-          relative();
         }
         uint32_t pf[2][NT][2];  // B operand: keys 2 qd, 2 qd + 1 (and + 8) of column g
 #pragma unroll
@@ -642,6 +645,16 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           lds_words(sb + (2 * qd + 1) * 2 * NC, w1);
           lds_words(sb + (2 * qd + 8) * 2 * NC, w2);
           lds_words(sb + (2 * qd + 9) * 2 * NC, w3);
+          if (partial) {  // the scale of a key that no column sees may be anything: zero times it must stay zero
+            const int k0 = u * I4_UNIT + mt * 16 + 2 * qd, lim = (lost >> mt & 1) ? 0 : see0 + rows - 1;
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i) {
+              if (k0 >= lim) w0[i] = 0;
+              if (k0 + 1 >= lim) w1[i] = 0;
+              if (k0 + 8 >= lim) w2[i] = 0;
+              if (k0 + 9 >= lim) w3[i] = 0;
+            }
+          }
 #pragma unroll
           for (int cp = 0; cp < NC / 2; ++cp) {
             uint32_t r[4];
@@ -654,18 +667,17 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
               i4_expand(r[2 * x + 1], b);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint32_t off = i & 1 ? 0x4e004e00u : 0x5c205c20u;  // 24, 264
-                a[i] = hsub2(a[i], off);
-                b[i] = hsub2(b[i], off);
+                a[i] = hsub2(a[i], i & 1 ? I4_OFF_ODD : I4_OFF_EVEN);
+                b[i] = hsub2(b[i], i & 1 ? I4_OFF_ODD : I4_OFF_EVEN);
               }
               const uint32_t s01 = __byte_perm(w0[cp], w1[cp], x ? 0x7632 : 0x5410);
               const uint32_t s89 = __byte_perm(w2[cp], w3[cp], x ? 0x7632 : 0x5410);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 uint32_t b0 = hmul2(pf[mt][nt][0], s01), b1 = hmul2(pf[mt][nt][1], s89);
-                if (partial) {  // a masked key's scale may be anything: its weight is zero, not zero times that
+                if (VARLEN && partial) {  // likewise the scale of a key that this column does not see
                   const int k0 = u * I4_UNIT + mt * 16 + 2 * qd;
-                  const int lim = (lost >> mt) & 1 ? 0 : limB[nt];
+                  const int lim = (lost >> mt) & 1 ? 0 : see0 + rowB(nt);
                   b0 &= (k0 < lim ? 0xffffu : 0u) | (k0 + 1 < lim ? 0xffff0000u : 0u);
                   b1 &= (k0 + 8 < lim ? 0xffffu : 0u) | (k0 + 9 < lim ? 0xffff0000u : 0u);
                 }
@@ -676,8 +688,11 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           }
         }
         __syncwarp();  // every lane has read the stage
-        if (++stage == STAGES) stage = 0;
-        produce();
+        produce(stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
       // ---- the item's end, or the range's
       const bool starts = pos == base, finishes = item_end <= u1;
@@ -691,14 +706,14 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
+          const int row = rowB(nt), head = nt * 8 + g - row * p.group;
           __nv_bfloat16* dst =
-              p.out + (static_cast<long long>(w.seq.q0 + row0 + rowB[nt]) * p.num_q_heads + w.h * p.group +
-                       headB[nt]) * D + 2 * qd;
+              p.out + (static_cast<long long>(w.seq.q0 + row0 + row) * p.num_q_heads + w.h * p.group + head) * D + 2 * qd;
 #pragma unroll
           for (int k = 0; k < 2 * NC; ++k) {
             const uint32_t a = movmatrix_trans(pack_bf16x2(o[k][nt][0] * i0, o[k][nt][1] * i1));
             const uint32_t b = movmatrix_trans(pack_bf16x2(o[k][nt][2] * i0, o[k][nt][3] * i1));
-            if (rowB[nt] < rows) {
+            if (row < rows) {
               *reinterpret_cast<uint32_t*>(dst + k * 16) = a;
               *reinterpret_cast<uint32_t*>(dst + k * 16 + 8) = b;
             }
@@ -722,33 +737,42 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
               rec_out[COLS * (D + 1) + col] = l[nt][j];
             }
           }
-        end.row[slot] = w.seq.q0 + row0;
-        end.rows[slot] = rows;
-        end.h[slot] = w.h;
-        end.first[slot] = base;
-        end.units[slot] = w.seq.units;
-        if (slot == 0) {
-          end.has0 = 1;
-          end.on0 = !finishes;
-        } else {
-          end.has1 = 1;
+        WarpEnd& we = ends[warp];
+        if (lane == 0) {
+          we.row[slot] = w.seq.q0 + row0;
+          we.rows[slot] = rows;
+          we.h[slot] = w.h;
+          we.first[slot] = base;
+          we.units[slot] = w.seq.units;
+          if (slot == 0) {
+            we.has0 = 1;
+            we.on0 = !finishes;
+          } else {
+            we.has1 = 1;
+          }
         }
       }
       pos = min(item_end, u1);
       if (pos < u1) {
-        base = item_end;
-        i4_next(p, w);
+        __syncwarp();
+        if (lane == 0) {
+          ws.cbase = item_end;
+          i4_next(p, ws.c);
+        }
+        __syncwarp();
       }
     }
     if (dead) {  // a copy did not land in time: report it, and give those in flight as long again
       if (lane == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_TIMEOUT));
       for (; flying > 0; --flying) {
-        (void)mbar_wait(bar + stage, (phases >> stage) & 1);
-        if (++stage == STAGES) stage = 0;
+        (void)mbar_wait(bar + stage, phase);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
     }
   }
-  if (lane == 0) ends[warp] = end;
   __syncthreads();
 
   // ---- merge the CTA's pieces.  Chain e: the item the CTA's range starts inside
@@ -838,7 +862,7 @@ size_t int4_workspace(int head_dim, int num_sms) {
   return (n + 255) / 256 * 256;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool VARLEN>
 int launch_int4(Int4Params& p, void* workspace, cudaStream_t stream, int num_sms) {
   using C = I4<D, NT>;
   p.rows_per_item = p.query_start ? C::COLS / p.group : 1;
@@ -851,7 +875,7 @@ int launch_int4(Int4Params& p, void* workspace, cudaStream_t stream, int num_sms
       ready,
       [](int) {
         const cudaError_t e =
-            cudaFuncSetAttribute(int4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            cudaFuncSetAttribute(int4_kernel<D, NT, VARLEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         return e == cudaSuccess ? 1 : cuda_fail(e, "cudaFuncSetAttribute");
       },
       &done);
@@ -866,7 +890,7 @@ int launch_int4(Int4Params& p, void* workspace, cudaStream_t stream, int num_sms
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return check_launch(cudaLaunchKernelEx(&cfg, int4_kernel<D, NT>, p), "int4_kernel launch");
+  return check_launch(cudaLaunchKernelEx(&cfg, int4_kernel<D, NT, VARLEN>, p), "int4_kernel launch");
 }
 
 int run_int4(void* out, const void* q, const int32_t* query_start, const void* k_cache, const void* v_cache,
@@ -910,12 +934,13 @@ int run_int4(void* out, const void* q, const int32_t* query_start, const void* k
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // One n-tile of columns where 8 hold a row's heads and the call has one row per sequence; two for wider groups,
   // and for several rows, which then share each unpacked key.
-  const bool two = group > 8 || query_start;
-  if (head_dim == 64)
-    return two ? launch_int4<64, 2>(p, workspace, st, di.num_sms) : launch_int4<64, 1>(p, workspace, st, di.num_sms);
-  if (head_dim == 128)
-    return two ? launch_int4<128, 2>(p, workspace, st, di.num_sms) : launch_int4<128, 1>(p, workspace, st, di.num_sms);
-  return launch_int4<256, 1>(p, workspace, st, di.num_sms);
+  const auto launch = [&](auto kernel) { return kernel(p, workspace, st, di.num_sms); };
+  if (query_start)
+    return launch(head_dim == 64 ? launch_int4<64, 2, true>
+                                 : head_dim == 128 ? launch_int4<128, 2, true> : launch_int4<256, 1, true>);
+  if (group > 8) return launch(head_dim == 64 ? launch_int4<64, 2, false> : launch_int4<128, 2, false>);
+  return launch(head_dim == 64 ? launch_int4<64, 1, false>
+                               : head_dim == 128 ? launch_int4<128, 1, false> : launch_int4<256, 1, false>);
 }
 
 }  // namespace
