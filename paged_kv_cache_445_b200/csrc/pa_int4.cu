@@ -34,6 +34,8 @@
 // Pieces of an item cut between warps go to the workspace as (O, m, l); the
 // CTA merges those of its own warps, and the last CTA to bring a piece of an
 // item merges the CTAs', in order.  No thread waits for another CTA.
+#include <type_traits>
+
 #include "pa_device.cuh"
 #include "pa_int4.cuh"
 #include "pa_internal.h"
@@ -55,7 +57,8 @@ struct I4 {
   static constexpr int HALF_BYTES = I4_UNIT * (D * 9 / 16); // K (or V) of a unit
   static constexpr int STAGE_BYTES = 2 * HALF_BYTES;
   static constexpr int STAGES = 221184 / WARPS / STAGE_BYTES;
-  static constexpr int PIECE = COLS * (D + 2);              // floats: O [COLS][D], m [COLS], l [COLS]
+  // a piece, in floats, as the lanes hold it: O [2 NC][NT] and (m, m, l, l) [NT] of 32 lanes x 4
+  static constexpr int PIECE = (2 * NC + 1) * NT * 128;
   static constexpr int RING_BYTES = WARPS * STAGES * STAGE_BYTES;
   static constexpr int SMEM = RING_BYTES + 8 * I4_BUCKETS + 8 * WARPS * STAGES + 512;
 };
@@ -147,12 +150,30 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // 8 codes (nibbles of the two halves of w) -> 4 fp16 pairs: 1024 + u in 0 and 2, 64 + u in 1 and 3 (the nibble
 // lies in the mantissa where its lowest bit is worth one: five operations).
-__device__ __forceinline__ void i4_expand(uint32_t w, uint32_t (&h)[4]) {
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+  return d;
+}
+// The two masks and the two exponents, in registers: an instruction holds one constant of its own, no more.
+struct Magic {
+  uint32_t even, odd;
+};
+__device__ __forceinline__ void i4_expand(uint32_t w, const Magic& e, uint32_t (&h)[4]) {
   const uint32_t b = w >> 8;
-  h[0] = (w & 0x000f000fu) | 0x64006400u;
-  h[1] = (w & 0x00f000f0u) | 0x54005400u;
-  h[2] = (b & 0x000f000fu) | 0x64006400u;
-  h[3] = (b & 0x00f000f0u) | 0x54005400u;
+  h[0] = and_or(w, 0x000f000fu, e.even);
+  h[1] = and_or(w, 0x00f000f0u, e.odd);
+  h[2] = and_or(b, 0x000f000fu, e.even);
+  h[3] = and_or(b, 0x00f000f0u, e.odd);
+}
+// D = A B + C with C in registers of its own (a chunk's constant part is used again and again).
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 constexpr uint32_t I4_OFF_EVEN = 0x64086408u, I4_OFF_ODD = 0x54805480u;    // 1024 + 8, 64 + 8
 constexpr uint32_t I4_NEG_EVEN = 0xe408e408u, I4_NEG_ODD = 0xd480d480u;
@@ -182,66 +203,52 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
   }
 }
 
-// Merge n pieces into one column: piece(k) is the k-th piece's record (or nullptr).  A warp
-// takes one column; lane i the dims 4 i .. 4 i + 3 of each 128.  If `final`,
-// writes the normalised row to out (bf16), else a piece record to dst.
-template <int D, int COLS, class Piece>
-__device__ __forceinline__ void merge_column(Piece piece, int n, int col, int lane, __nv_bfloat16* out, float* dst) {
-  float m = I4_NO_MAX;
-  for (int k = lane; k < n; k += 32) {
-    const float* r = piece(k);
-    if (r && __ldcg(r + COLS * (D + 1) + col) != 0.f) m = fmaxf(m, __ldcg(r + COLS * D + col));
+// Merge the k-th pair of O tiles of n pieces (piece(i): the i-th record, or nullptr): a warp takes a pair, each lane
+// the elements and the columns it would hold in the main loop.  One pass with a running maximum; a few pieces' loads
+// are in flight together.
+template <int D, int NT, class Piece>
+__device__ __forceinline__ void merge_pair(Piece piece, int n, int k, int lane, float (&o)[2][NT][4], float (&m)[NT][2],
+                                           float (&l)[NT][2]) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = I4_NO_MAX;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[0][nt][i] = o[1][nt][i] = 0.f;
   }
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float4* r = reinterpret_cast<const float4*>(piece(i));
+    if (!r) continue;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
-  constexpr int PARTS = (D + 127) / 128;
-  float4 acc[PARTS];
+    for (int nt = 0; nt < NT; ++nt) {
+      const float4 ml = __ldcg(r + (D / 16 * NT + nt) * 32 + lane);
+      const float4 x = __ldcg(r + (2 * k * NT + nt) * 32 + lane);
+      const float4 y = __ldcg(r + ((2 * k + 1) * NT + nt) * 32 + lane);
+      const float mk[2] = {ml.x, ml.y}, lk[2] = {ml.z, ml.w};
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    float w = 0.f;
-    if (k0 + lane < n) {
-      const float* r = piece(k0 + lane);
-      const float lk = r ? __ldcg(r + COLS * (D + 1) + col) : 0.f;
-      if (lk != 0.f) {  // (a NaN sum stays)
-        w = fast_exp2(__ldcg(r + COLS * D + col) - m);
-        l += lk * w;
+      for (int j = 0; j < 2; ++j) {
+        if (lk[j] == 0.f) continue;  // no key of this column here (a NaN sum goes on)
+        const float mn = fmaxf(m[nt][j], mk[j]);
+        const float a = fast_exp2(m[nt][j] - mn), b = fast_exp2(mk[j] - mn);
+        m[nt][j] = mn;
+        l[nt][j] = l[nt][j] * a + lk[j] * b;
+        o[0][nt][j] = o[0][nt][j] * a + (j ? x.y : x.x) * b;
+        o[0][nt][j + 2] = o[0][nt][j + 2] * a + (j ? x.w : x.z) * b;
+        o[1][nt][j] = o[1][nt][j] * a + (j ? y.y : y.x) * b;
+        o[1][nt][j + 2] = o[1][nt][j + 2] * a + (j ? y.w : y.z) * b;
       }
     }
-    const int cnt = min(32, n - k0);
-    for (int k = 0; k < cnt; ++k) {
-      const float wk = __shfl_sync(FULL_MASK, w, k);
-      if (wk == 0.f) continue;
-      const float* r = piece(k0 + k) + col * D;
-#pragma unroll
-      for (int i = 0; i < PARTS; ++i)
-        if (D >= 128 || lane < D / 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(r + i * 128 + lane * 4));
-          acc[i].x += wk * x.x;
-          acc[i].y += wk * x.y;
-          acc[i].z += wk * x.z;
-          acc[i].w += wk * x.w;
-        }
-    }
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(FULL_MASK, l, o);
-  if (out) {
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int i = 0; i < PARTS; ++i)
-      if (D >= 128 || lane < D / 4)
-        *reinterpret_cast<uint2*>(out + i * 128 + lane * 4) =
-            make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
-  } else {
-#pragma unroll
-    for (int i = 0; i < PARTS; ++i)
-      if (D >= 128 || lane < D / 4) *reinterpret_cast<float4*>(dst + col * D + i * 128 + lane * 4) = acc[i];
-    if (lane == 0) {
-      dst[COLS * D + col] = m;
-      dst[COLS * (D + 1) + col] = l;
-    }
+}
+
+// Store one 16-dim tile of O, scaled, to the column's row (dst: its place for this lane, dims 2 qd of the tile).
+__device__ __forceinline__ void store_tile(__nv_bfloat16* dst, const float (&o)[4], float i0, float i1, bool on) {
+  const uint32_t a = movmatrix_trans(pack_bf16x2(o[0] * i0, o[1] * i1));
+  const uint32_t b = movmatrix_trans(pack_bf16x2(o[2] * i0, o[3] * i1));
+  if (on) {
+    *reinterpret_cast<uint32_t*>(dst) = a;
+    *reinterpret_cast<uint32_t*>(dst + 8) = b;
   }
 }
 
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   __shared__ WarpEnd ends[WARPS];
   __shared__ WarpState walks[WARPS];
   __shared__ int sh_merge;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL_MASK, tid >> 5, 0);  // (one value to the compiler)
   const int g = lane >> 2, qd = lane & 3;
   const int bs = 1 << p.block_shift;
 
@@ -349,13 +356,20 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
     colrow[nt] = (nt * 8 + g) / p.group | (nt * 8 + 2 * qd) / p.group << 8 | (nt * 8 + 2 * qd + 1) / p.group << 16;
   const auto rowB = [&](int nt) { return colrow[nt] & 0xff; };
   const auto rowA = [&](int nt, int j) { return colrow[nt] >> (8 + 8 * j) & 0xff; };
+  // where column g + 8 nt of an item's output starts for this lane
+  const auto out_place = [&](int row, int h, int nt) {
+    const int r = rowB(nt), head = nt * 8 + g - r * p.group;
+    return p.out + (static_cast<long long>(row + r) * p.num_q_heads + h * p.group + head) * D + 2 * qd;
+  };
   // ldmatrix: lane i gives row (i & 7) + 8 ((i >> 3) & 1) of chunk i >> 4 (+ 2 per step)
   const uint32_t code_at = int4_code_offset<D>((lane & 7) + (lane & 8), lane >> 4);
-  uint8_t* ring = smem + warp * STAGES * C::STAGE_BYTES;
+  const uint32_t ring_at = smem_u32(smem) + warp * STAGES * C::STAGE_BYTES;
   uint64_t* bar = bars + warp * STAGES;
   const int rec = int4_record_bytes(bs, D);
   const int unit_shift = 5 - p.block_shift;  // log2 of the blocks of a unit
   WarpState& ws = walks[warp];
+  Magic magic{0x64006400u, 0x54005400u};
+  asm volatile("" : "+r"(magic.even), "+r"(magic.odd));
 
   if (u0 < u1) {
     // ---- find the item of u0
@@ -389,12 +403,11 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
     // ---- producer: the same walk, ahead by up to STAGES units
     int pu = static_cast<int>(u0 - ws.pbase), pend = static_cast<int>(min(static_cast<long long>(ws.p.live), u1 - ws.pbase));
     int entries = (ws.p.seq.ctx + bs - 1) >> p.block_shift, head_off = ws.p.h * rec;
-    int ids = 0, ids_from = INT32_MAX;  // block IDs of 32 table entries from ids_from on, one per lane
+    int ids = 0, ids_from = INT32_MAX;  // block IDs of 32 table entries from ids_from on, one per lane; -1: no such block
     int flying = 0;                     // units loaded and not yet waited for
     unsigned bad = 0;                   // two bits per stage: blocks of its unit that were not loaded
-    // lanes 0 .. 3 copy K and V (lane & 1) of the unit's first and second block (lane >> 1)
-    const uint8_t* cache = (lane & 1 ? p.v_cache : p.k_cache);
-    const uint32_t copy_to = smem_u32(ring) + (lane & 1) * C::HALF_BYTES + (lane >> 1 & 1) * rec;
+    const uint32_t stride = p.num_kv_heads * rec;
+    const long long k_to_v = p.v_cache - p.k_cache;
 
     const auto produce = [&](int to) {
       if (pu >= pend) {
@@ -418,28 +431,50 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         ids_from = INT32_MAX;
       }
       const int entry = pu << unit_shift;
-      if (entry < ids_from || entry >= ids_from + 32) {
+      if (static_cast<unsigned>(entry - ids_from) >= 32u) {
         ids_from = entry;
         ids = entry + lane < entries
                   ? __ldg(p.block_tables + static_cast<long long>(ws.p.s) * p.max_blocks + entry + lane)
                   : -1;
+        if (ids >= p.num_blocks) ids = -1;
       }
-      const int mine = entry + (lane >> 1 & unit_shift);  // (unit_shift is 1 or 0: the second block, or the first again)
-      const int id = __shfl_sync(FULL_MASK, ids, mine - ids_from);
-      const bool in = lane < 2 << unit_shift && mine < entries;
-      const bool ok = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
-      const unsigned go = __ballot_sync(FULL_MASK, in && ok);
-      const unsigned lost = __ballot_sync(FULL_MASK, in && !ok);
+      const int id0 = __shfl_sync(FULL_MASK, ids, entry - ids_from);
+      const int id1 = __shfl_sync(FULL_MASK, ids, entry + unit_shift - ids_from);  // bs 32: the same again
+      const uint32_t dst = ring_at + to * C::STAGE_BYTES;
+      uint64_t* fb = bar + to;
       bad &= ~(3u << (2 * to));
-      if (lost) {
-        bad |= (unit_shift ? (lost & 1) | (lost >> 1 & 2) : 3u) << (2 * to);
-        if (lane == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
+      if ((id0 | id1) >= 0) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
+          const uint8_t* k0 = p.k_cache + static_cast<unsigned long long>(id0) * stride + head_off;
+          bulk_load(dst, k0, rec, fb);
+          bulk_load(dst + C::HALF_BYTES, k0 + k_to_v, rec, fb);
+          if (unit_shift) {
+            const uint8_t* k1 = p.k_cache + static_cast<unsigned long long>(id1) * stride + head_off;
+            bulk_load(dst + rec, k1, rec, fb);
+            bulk_load(dst + C::HALF_BYTES + rec, k1 + k_to_v, rec, fb);
+          }
+        }
+      } else {  // the last block of a context, or a bad ID
+        const bool in1 = unit_shift && entry + 1 < entries;
+        const unsigned lost = (id0 < 0 ? (unit_shift ? 1u : 3u) : 0u) | (in1 && id1 < 0 ? 2u : 0u);
+        bad |= lost << (2 * to);
+        if (lane == 0) {
+          if (lost) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
+          const bool two = unit_shift && id1 >= 0;
+          mbar_arrive_expect_tx(fb, 2 * rec * ((id0 >= 0 ? 1 : 0) + (two ? 1 : 0)));
+          if (id0 >= 0) {
+            const uint8_t* k0 = p.k_cache + static_cast<unsigned long long>(id0) * stride + head_off;
+            bulk_load(dst, k0, rec, fb);
+            bulk_load(dst + C::HALF_BYTES, k0 + k_to_v, rec, fb);
+          }
+          if (two) {
+            const uint8_t* k1 = p.k_cache + static_cast<unsigned long long>(id1) * stride + head_off;
+            bulk_load(dst + rec, k1, rec, fb);
+            bulk_load(dst + C::HALF_BYTES + rec, k1 + k_to_v, rec, fb);
+          }
+        }
       }
-      if (lane == 0) mbar_arrive_expect_tx(bar + to, __popc(go) * rec);
-      __syncwarp();
-      if (in && ok)
-        bulk_load(copy_to + to * C::STAGE_BYTES, cache + static_cast<long long>(id) * p.num_kv_heads * rec + head_off, rec,
-                  bar + to);
       ++flying;
       ++pu;
     };
@@ -496,17 +531,16 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         fac[nt][1] = __shfl_sync(FULL_MASK, f, 8 * qd + 4);
       }
       // the constant part of each chunk's scores: -1032 or -72 times q, summed
-      float cst[NC][NT][2];
+      float cst[NC][NT][4];
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          float (&d)[4] = cst[c][nt];
+          d[0] = d[1] = d[2] = d[3] = 0.f;
 #pragma unroll
           for (int k = 2 * c; k < 2 * c + 2; ++k)
             mma_f16_16816(d, I4_NEG_EVEN, I4_NEG_EVEN, I4_NEG_ODD, I4_NEG_ODD, qf[k][nt][0], qf[k][nt][1]);
-          cst[c][nt][0] = d[0];
-          cst[c][nt][1] = d[1];
         }
       float o[2 * NC][NT][4];
       float l[NT][2], m[NT][2];
@@ -521,16 +555,8 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       }
       unsigned fresh = (1u << 2 * NT) - 1;  // columns without a score so far: their reference is not one yet
 
-#pragma unroll 1
-      for (int u = first; u < last; ++u) {
-        const uint32_t ka = smem_u32(ring) + stage * C::STAGE_BYTES;
-        const unsigned lost = (bad >> (2 * stage)) & 3u;
-        if (!__all_sync(FULL_MASK, !dead && mbar_wait(bar + stage, phase))) {
-          dead = true;
-          break;
-        }
-        --flying;
-        const bool partial = u * I4_UNIT + I4_UNIT > see0 || lost;  // some key is masked for some column
+      const auto unit = [&](auto partial, int u, uint32_t ka, unsigned lost) {
+        constexpr bool PARTIAL = decltype(partial)::value;
 
         // ---- scores of 32 keys
         float y[2][NT][4];
@@ -542,10 +568,6 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           lds_words(sb + g * 2 * NC, sc0);
           lds_words(sb + (g + 8) * 2 * NC, sc1);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[mt][nt][i] = 0.f;
-#pragma unroll
           for (int cp = 0; cp < NC / 2; ++cp) {
             uint32_t r[4];
             ldsm_x4(rb + (code_at ^ (cp * 32)), r[0], r[1], r[2], r[3]);
@@ -553,18 +575,19 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
             for (int x = 0; x < 2; ++x) {  // chunk 2 cp + x: rows 0-7 in r[2 x], rows 8-15 in r[2 x + 1]
               const int c = 2 * cp + x;
               uint32_t a[4], b[4];
-              i4_expand(r[2 * x], a);
-              i4_expand(r[2 * x + 1], b);
+              i4_expand(r[2 * x], magic, a);
+              i4_expand(r[2 * x + 1], magic, b);
               const float f0 = half_of(sc0[cp], x), f1 = half_of(sc1[cp], x);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                float d[4] = {cst[c][nt][0], cst[c][nt][1], cst[c][nt][0], cst[c][nt][1]};
-                mma_f16_16816(d, a[0], b[0], a[1], b[1], qf[2 * c][nt][0], qf[2 * c][nt][1]);
+                float d[4];
+                mma_f16_from(d, a[0], b[0], a[1], b[1], qf[2 * c][nt][0], qf[2 * c][nt][1], cst[c][nt]);
                 mma_f16_16816(d, a[2], b[2], a[3], b[3], qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
-                y[mt][nt][0] = fmaf(d[0], f0, y[mt][nt][0]);
-                y[mt][nt][1] = fmaf(d[1], f0, y[mt][nt][1]);
-                y[mt][nt][2] = fmaf(d[2], f1, y[mt][nt][2]);
-                y[mt][nt][3] = fmaf(d[3], f1, y[mt][nt][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float f = i < 2 ? f0 : f1;
+                  y[mt][nt][i] = c == 0 ? d[i] * f : fmaf(d[i], f, y[mt][nt][i]);
+                }
               }
             }
           }
@@ -578,9 +601,9 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               y[mt][nt][i] = fmaf(y[mt][nt][i], fac[nt][i & 1], -m[nt][i & 1]);
-              if (!partial) top = fmaxf(top, y[mt][nt][i]);
+              if (!PARTIAL) top = fmaxf(top, y[mt][nt][i]);
             }
-        if (partial) {
+        if (PARTIAL) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -645,7 +668,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           lds_words(sb + (2 * qd + 1) * 2 * NC, w1);
           lds_words(sb + (2 * qd + 8) * 2 * NC, w2);
           lds_words(sb + (2 * qd + 9) * 2 * NC, w3);
-          if (partial) {  // the scale of a key that no column sees may be anything: zero times it must stay zero
+          if (PARTIAL) {  // the scale of a key that no column sees may be anything: zero times it must stay zero
             const int k0 = u * I4_UNIT + mt * 16 + 2 * qd, lim = (lost >> mt & 1) ? 0 : see0 + rows - 1;
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) {
@@ -663,8 +686,8 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
             for (int x = 0; x < 2; ++x) {  // chunk 2 cp + x: keys 0-7 in r[2 x], keys 8-15 in r[2 x + 1]
               const int c = 2 * cp + x;
               uint32_t a[4], b[4];
-              i4_expand(r[2 * x], a);
-              i4_expand(r[2 * x + 1], b);
+              i4_expand(r[2 * x], magic, a);
+              i4_expand(r[2 * x + 1], magic, b);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 a[i] = hsub2(a[i], i & 1 ? I4_OFF_ODD : I4_OFF_EVEN);
@@ -675,7 +698,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 uint32_t b0 = hmul2(pf[mt][nt][0], s01), b1 = hmul2(pf[mt][nt][1], s89);
-                if (VARLEN && partial) {  // likewise the scale of a key that this column does not see
+                if (VARLEN && PARTIAL) {  // likewise the scale of a key that this column does not see
                   const int k0 = u * I4_UNIT + mt * 16 + 2 * qd;
                   const int lim = (lost >> mt) & 1 ? 0 : see0 + rowB(nt);
                   b0 &= (k0 < lim ? 0xffffu : 0u) | (k0 + 1 < lim ? 0xffff0000u : 0u);
@@ -687,6 +710,22 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
             }
           }
         }
+      };
+
+#pragma unroll 1
+      for (int u = first; u < last; ++u) {
+        const uint32_t ka = ring_at + stage * C::STAGE_BYTES;
+        const unsigned lost = (bad >> (2 * stage)) & 3u;
+        if (!__all_sync(FULL_MASK, !dead && mbar_wait(bar + stage, phase))) {
+          dead = true;
+          break;
+        }
+        --flying;
+        // (some key is masked for some column, or none is: two copies of the body)
+        if (u * I4_UNIT + I4_UNIT > see0 || lost)
+          unit(std::true_type{}, u, ka, lost);
+        else
+          unit(std::false_type{}, u, ka, 0u);
         __syncwarp();  // every lane has read the stage
         produce(stage);
         if (++stage == STAGES) {
@@ -706,37 +745,20 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
-          const int row = rowB(nt), head = nt * 8 + g - row * p.group;
-          __nv_bfloat16* dst =
-              p.out + (static_cast<long long>(w.seq.q0 + row0 + row) * p.num_q_heads + w.h * p.group + head) * D + 2 * qd;
+          __nv_bfloat16* dst = out_place(w.seq.q0 + row0, w.h, nt);
 #pragma unroll
-          for (int k = 0; k < 2 * NC; ++k) {
-            const uint32_t a = movmatrix_trans(pack_bf16x2(o[k][nt][0] * i0, o[k][nt][1] * i1));
-            const uint32_t b = movmatrix_trans(pack_bf16x2(o[k][nt][2] * i0, o[k][nt][3] * i1));
-            if (row < rows) {
-              *reinterpret_cast<uint32_t*>(dst + k * 16) = a;
-              *reinterpret_cast<uint32_t*>(dst + k * 16 + 8) = b;
-            }
-          }
+          for (int k = 0; k < 2 * NC; ++k) store_tile(dst + k * 16, o[k][nt], i0, i1, rowB(nt) < rows);
         }
       } else {
         const int slot = starts ? 1 : 0;
-        float* rec_out = piece0 + slot * C::PIECE;
+        float4* rec_out = reinterpret_cast<float4*>(piece0 + slot * C::PIECE) + lane;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int col = nt * 8 + 2 * qd + j;
-#pragma unroll
-            for (int k = 0; k < 2 * NC; ++k) {
-              rec_out[col * D + k * 16 + g] = o[k][nt][j];
-              rec_out[col * D + k * 16 + 8 + g] = o[k][nt][j + 2];
-            }
-            if (g == 0) {
-              rec_out[COLS * D + col] = m[nt][j];
-              rec_out[COLS * (D + 1) + col] = l[nt][j];
-            }
-          }
+          for (int k = 0; k < 2 * NC; ++k)
+            rec_out[(k * NT + nt) * 32] = make_float4(o[k][nt][0], o[k][nt][1], o[k][nt][2], o[k][nt][3]);
+          rec_out[(2 * NC * NT + nt) * 32] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
+        }
         WarpEnd& we = ends[warp];
         if (lane == 0) {
           we.row[slot] = w.seq.q0 + row0;
@@ -779,6 +801,15 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   // of (e = 0), or the one that starts in warp e - 1 and goes on past it.
   float* cta_piece = p.cta_pieces + static_cast<long long>(blockIdx.x) * 2 * C::PIECE;
   const float* pieces = p.warp_pieces + static_cast<long long>(blockIdx.x) * WARPS * 2 * C::PIECE;
+  const auto finish = [&](const float (&o)[2][NT][4], const float (&l)[NT][2], int k, int row, int rows, int h) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
+      __nv_bfloat16* dst = out_place(row, h, nt) + k * 32;
+      store_tile(dst, o[0][nt], i0, i1, rowB(nt) < rows);
+      store_tile(dst + 16, o[1][nt], i0, i1, rowB(nt) < rows);
+    }
+  };
   int job = 0;
   for (int e = 0; e <= WARPS; ++e) {
     if (e == 0 ? !ends[0].has0 : !ends[e - 1].has1) continue;
@@ -791,18 +822,26 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
     const WarpEnd& we = ends[w0];
     const long long first = we.first[sl], after = first + we.units[sl];
     const bool inside = first >= c0 && after <= c0 + cn;
-    const int cols = we.rows[sl] * p.group;
     const auto piece = [&](int k) -> const float* {
       if (k > 0 && !ends[w0 + k].has0) return nullptr;  // a warp without units
       return pieces + (static_cast<long long>(w0 + k) * 2 + (k == 0 ? sl : 0)) * C::PIECE;
     };
     const int n = w1 - w0 + 1;
-    for (int col = 0; col < cols; ++col, ++job) {
+    for (int k = 0; k < NC; ++k, ++job) {
       if (job % WARPS != warp) continue;
-      const int r = col / p.group, hh = col - r * p.group;
-      __nv_bfloat16* out =
-          p.out + (static_cast<long long>(we.row[sl] + r) * p.num_q_heads + we.h[sl] * p.group + hh) * D;
-      merge_column<D, COLS>(piece, n, col, lane, inside ? out : nullptr, cta_piece + (e == 0 ? 0 : 1) * C::PIECE);
+      float o[2][NT][4], m[NT][2], l[NT][2];
+      merge_pair<D, NT>(piece, n, k, lane, o, m, l);
+      if (inside) {
+        finish(o, l, k, we.row[sl], we.rows[sl], we.h[sl]);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(cta_piece + (e == 0 ? 0 : 1) * C::PIECE) + lane;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          dst[(2 * k * NT + nt) * 32] = make_float4(o[0][nt][0], o[0][nt][1], o[0][nt][2], o[0][nt][3]);
+          dst[((2 * k + 1) * NT + nt) * 32] = make_float4(o[1][nt][0], o[1][nt][1], o[1][nt][2], o[1][nt][3]);
+          if (k == 0) dst[(2 * NC * NT + nt) * 32] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
+        }
+      }
     }
   }
   // ---- pieces of items that cross CTAs: count them in; the last CTA merges
@@ -830,15 +869,13 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
     }
     __syncthreads();
     if (sh_merge) {
-      const int cols = we.rows[e] * p.group;
       const auto piece = [&](int k) -> const float* {  // the first CTA's piece starts in it (slot 1), the others' came from before (slot 0)
         return p.cta_pieces + (static_cast<long long>(f + k) * 2 + (k == 0 ? 1 : 0)) * C::PIECE;
       };
-      for (int col = warp; col < cols; col += WARPS) {
-        const int r = col / p.group, hh = col - r * p.group;
-        merge_column<D, COLS>(
-            piece, n, col, lane,
-            p.out + (static_cast<long long>(we.row[e] + r) * p.num_q_heads + we.h[e] * p.group + hh) * D, nullptr);
+      for (int k = warp; k < NC; k += WARPS) {
+        float o[2][NT][4], m[NT][2], l[NT][2];
+        merge_pair<D, NT>(piece, n, k, lane, o, m, l);
+        finish(o, l, k, we.row[e], we.rows[e], we.h[e]);
       }
     }
     __syncthreads();
