@@ -44,23 +44,33 @@ namespace pa {
 
 namespace {
 
+#ifndef I4_W
+#define I4_W 12
+#endif
 constexpr int I4_UNIT = 32;        // keys
-constexpr int I4_BUCKETS = 512;    // prefix sums of the batch's units, of runs of sequences
+constexpr int I4_FEW = 6;             // pieces of an item across CTAs that one warp merges
+constexpr int I4_WARP_COUNTERS = 512; // counters: per CTA, then (from here) per warp
+constexpr size_t I4_COUNTER_BYTES = 4 * (512 + 512 * 16);
+#ifndef I4_PAD
+#define I4_PAD 1
+#endif
 constexpr float I4_NO_MAX = -3e38f; // maximum over no pieces
 
 template <int D, int NT>
 struct I4 {
   static constexpr int NC = D / 32;                         // chunks of a row
   static constexpr int COLS = 8 * NT;
-  static constexpr int WARPS = D * NT <= 128 ? 16 : 8;      // 128 or 255 registers a thread
+  static constexpr int WARPS = D * NT <= 128 ? I4_W : 8;      // 128 or 255 registers a thread
   static constexpr int THREADS = 32 * WARPS;
+  static constexpr int PER = WARPS > 8 ? 1 : 2;            // prefix sums of the batch's units, per thread
+  static constexpr int BUCKETS = THREADS * PER;            // of runs of sequences
   static constexpr int HALF_BYTES = I4_UNIT * (D * 9 / 16); // K (or V) of a unit
   static constexpr int STAGE_BYTES = 2 * HALF_BYTES;
   static constexpr int STAGES = 221184 / WARPS / STAGE_BYTES;
   // a piece, in floats, as the lanes hold it: O [2 NC][NT] and (m, m, l, l) [NT] of 32 lanes x 4
   static constexpr int PIECE = (2 * NC + 1) * NT * 128;
   static constexpr int RING_BYTES = WARPS * STAGES * STAGE_BYTES;
-  static constexpr int SMEM = RING_BYTES + 8 * I4_BUCKETS + 8 * WARPS * STAGES + 512;
+  static constexpr int SMEM = RING_BYTES + 8 * BUCKETS + 8 * WARPS * STAGES + 512;
 };
 
 struct Int4Params {
@@ -74,7 +84,7 @@ struct Int4Params {
   int num_seqs, num_rows, max_blocks, num_q_heads, num_kv_heads, group, rows_per_item, block_shift, num_blocks;
   float scale_log2;
   int* status;
-  int* counters;        // workspace: pieces brought per CTA that an item starts in; zero between calls
+  int* counters;        // workspace: pieces brought per CTA or warp that an item starts in; zero between calls
   float* warp_pieces;   // workspace: [CTA][warp][2]
   float* cta_pieces;    // workspace: [CTA][2]
 };
@@ -104,7 +114,7 @@ __device__ __forceinline__ SeqInfo i4_seq(const Int4Params& p, int s, int* bits 
     bad = PA_STATUS_BIT(PA_ERR_RANGE);
     i.ctx = 0;
   }
-  i.units = i.ctx > 0 && i.qlen > 0 ? (i.ctx + I4_UNIT - 1) / I4_UNIT : 0;
+  i.units = i.ctx > 0 && i.qlen > 0 ? (i.ctx + I4_UNIT - 1) / I4_UNIT + I4_PAD : 0;
   if (bits) *bits |= bad;
   return i;
 }
@@ -166,15 +176,6 @@ __device__ __forceinline__ void i4_expand(uint32_t w, const Magic& e, uint32_t (
   h[2] = and_or(b, 0x000f000fu, e.even);
   h[3] = and_or(b, 0x00f000f0u, e.odd);
 }
-// D = A B + C with C in registers of its own (a chunk's constant part is used again and again).
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                             uint32_t b0, uint32_t b1, const float (&c)[4]) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
 constexpr uint32_t I4_OFF_EVEN = 0x64086408u, I4_OFF_ODD = 0x54805480u;    // 1024 + 8, 64 + 8
 constexpr uint32_t I4_NEG_EVEN = 0xe408e408u, I4_NEG_ODD = 0xd480d480u;
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
@@ -219,16 +220,16 @@ __device__ __forceinline__ void merge_pair(Piece piece, int n, int k, int lane, 
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
     const float4* r = reinterpret_cast<const float4*>(piece(i));
-    if (!r) continue;
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float4 ml = __ldcg(r + (D / 16 * NT + nt) * 32 + lane);
-      const float4 x = __ldcg(r + (2 * k * NT + nt) * 32 + lane);
-      const float4 y = __ldcg(r + ((2 * k + 1) * NT + nt) * 32 + lane);
-      const float mk[2] = {ml.x, ml.y}, lk[2] = {ml.z, ml.w};
+      const float4 ml = r ? __ldcg(r + (D / 16 * NT + nt) * 32 + lane) : none;
+      const float4 x = r ? __ldcg(r + (2 * k * NT + nt) * 32 + lane) : none;
+      const float4 y = r ? __ldcg(r + ((2 * k + 1) * NT + nt) * 32 + lane) : none;
+      const float lk[2] = {ml.z, ml.w};
+      const float mk[2] = {lk[0] != 0.f ? ml.x : I4_NO_MAX, lk[1] != 0.f ? ml.y : I4_NO_MAX};  // no key: no maximum
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (lk[j] == 0.f) continue;  // no key of this column here (a NaN sum goes on)
         const float mn = fmaxf(m[nt][j], mk[j]);
         const float a = fast_exp2(m[nt][j] - mn), b = fast_exp2(mk[j] - mn);
         m[nt][j] = mn;
@@ -265,35 +266,42 @@ struct WarpEnd {
 struct WarpState {
   Walk c, p;               // consumer's and producer's place
   long long cbase, pbase;  // first units of their items
+  long long u0, u1;        // the warp's range
+  unsigned lost;           // two bits per stage: blocks of its unit that were not loaded
 };
 
 // VARLEN: several query rows per sequence (columns see different numbers of keys).
 template <int D, int NT, bool VARLEN>
 __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __grid_constant__ Int4Params p) {
   using C = I4<D, NT>;
-  constexpr int NC = C::NC, COLS = C::COLS, WARPS = C::WARPS, STAGES = C::STAGES;
+  constexpr int NC = C::NC, WARPS = C::WARPS, STAGES = C::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   long long* prefix = reinterpret_cast<long long*>(smem + C::RING_BYTES);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES + 8 * I4_BUCKETS);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES + 8 * C::BUCKETS);
   __shared__ long long scan[WARPS];
   __shared__ WarpEnd ends[WARPS];
   __shared__ WarpState walks[WARPS];
   __shared__ int sh_merge;
+  __shared__ int arrived[WARPS];  // pieces of the item inside the CTA that starts in each warp
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL_MASK, tid >> 5, 0);  // (one value to the compiler)
   const int g = lane >> 2, qd = lane & 3;
   const int bs = 1 << p.block_shift;
 
   if (lane == 0) {
+    arrived[warp] = 0;
     ends[warp].has0 = ends[warp].on0 = ends[warp].has1 = 0;
     for (int i = 0; i < STAGES; ++i) mbar_init(&bars[warp * STAGES + i], 1);
     fence_mbar_init();
   }
 
   grid_dependency_wait();
+#ifndef NOPDL
+  grid_launch_dependents();
+#endif
 
   // ---- units of the batch: prefix sums over runs of sequences
-  const int run = (p.num_seqs + I4_BUCKETS - 1) / I4_BUCKETS;
-  constexpr int PER = I4_BUCKETS / C::THREADS;
+  const int run = (p.num_seqs + C::BUCKETS - 1) / C::BUCKETS;
+  constexpr int PER = C::PER;
   long long mine[PER], sum = 0;
   int bits = 0;
 #pragma unroll
@@ -340,9 +348,15 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
   if (static_cast<int>(blockIdx.x) >= ctas) return;
   const auto cta_first = [&](long long c) { return c * (total / ctas) + (c < total % ctas ? c : total % ctas); };
+  const bool dense = total / ctas >= WARPS;  // every warp has a unit (else none has two)
   const auto cta_of = [&](long long u) {
     const long long q = total / ctas, r = total % ctas;
     return static_cast<int>(u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q);
+  };
+  const auto warp_of = [&](long long u) {  // of all the grid's warps
+    const int c = cta_of(u);
+    const long long f = cta_first(c);
+    return c * WARPS + static_cast<int>((u - f) * WARPS / (cta_first(c + 1) - f));
   };
   const long long c0 = cta_first(blockIdx.x), cn = cta_first(blockIdx.x + 1) - c0;
   // (rounded up: warp 0 always has a unit)
@@ -361,6 +375,24 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
     const int r = rowB(nt), head = nt * 8 + g - r * p.group;
     return p.out + (static_cast<long long>(row + r) * p.num_q_heads + h * p.group + head) * D + 2 * qd;
   };
+  const auto write_out = [&](const float (&o)[2 * NC][NT][4], const float (&l)[NT][2], int row, int rows, int h) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
+      __nv_bfloat16* dst = out_place(row, h, nt);
+#pragma unroll
+      for (int k = 0; k < 2 * NC; ++k) store_tile(dst + k * 16, o[k][nt], i0, i1, rowB(nt) < rows);
+    }
+  };
+  const auto finish = [&](const float (&o)[2][NT][4], const float (&l)[NT][2], int k, int row, int rows, int h) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
+      __nv_bfloat16* dst = out_place(row, h, nt) + k * 32;
+      store_tile(dst, o[0][nt], i0, i1, rowB(nt) < rows);
+      store_tile(dst + 16, o[1][nt], i0, i1, rowB(nt) < rows);
+    }
+  };
   // ldmatrix: lane i gives row (i & 7) + 8 ((i >> 3) & 1) of chunk i >> 4 (+ 2 per step)
   const uint32_t code_at = int4_code_offset<D>((lane & 7) + (lane & 8), lane >> 4);
   const uint32_t ring_at = smem_u32(smem) + warp * STAGES * C::STAGE_BYTES;
@@ -374,7 +406,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   if (u0 < u1) {
     // ---- find the item of u0
     {
-      int lo = 0, hi = I4_BUCKETS - 1;
+      int lo = 0, hi = C::BUCKETS - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (prefix[mid] > u0) hi = mid; else lo = mid + 1;
@@ -397,15 +429,17 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       if (lane == 0) {
         ws.c = ws.p = w;
         ws.cbase = ws.pbase = at + item * w.seq.units;
+        ws.u0 = u0;
+        ws.u1 = u1;
+        ws.lost = 0;
       }
       __syncwarp();
     }
     // ---- producer: the same walk, ahead by up to STAGES units
     int pu = static_cast<int>(u0 - ws.pbase), pend = static_cast<int>(min(static_cast<long long>(ws.p.live), u1 - ws.pbase));
     int entries = (ws.p.seq.ctx + bs - 1) >> p.block_shift, head_off = ws.p.h * rec;
+    unsigned odd = 0;                   // stages whose unit lacks a block
     int ids = 0, ids_from = INT32_MAX;  // block IDs of 32 table entries from ids_from on, one per lane; -1: no such block
-    int flying = 0;                     // units loaded and not yet waited for
-    unsigned bad = 0;                   // two bits per stage: blocks of its unit that were not loaded
     const uint32_t stride = p.num_kv_heads * rec;
     const long long k_to_v = p.v_cache - p.k_cache;
 
@@ -413,7 +447,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       if (pu >= pend) {
         do {
           const long long next = ws.pbase + ws.p.seq.units;
-          if (next >= u1) {
+          if (next >= ws.u1) {
             pend = 0;
             return;
           }
@@ -424,7 +458,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           }
           __syncwarp();
           pu = 0;
-          pend = static_cast<int>(min(static_cast<long long>(ws.p.live), u1 - next));
+          pend = static_cast<int>(min(static_cast<long long>(ws.p.live), ws.u1 - next));
         } while (pend <= 0);
         entries = (ws.p.seq.ctx + bs - 1) >> p.block_shift;
         head_off = ws.p.h * rec;
@@ -442,7 +476,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       const int id1 = __shfl_sync(FULL_MASK, ids, entry + unit_shift - ids_from);  // bs 32: the same again
       const uint32_t dst = ring_at + to * C::STAGE_BYTES;
       uint64_t* fb = bar + to;
-      bad &= ~(3u << (2 * to));
+      odd &= ~(1u << to);
       if ((id0 | id1) >= 0) {
         if (lane == 0) {
           mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
@@ -458,8 +492,9 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       } else {  // the last block of a context, or a bad ID
         const bool in1 = unit_shift && entry + 1 < entries;
         const unsigned lost = (id0 < 0 ? (unit_shift ? 1u : 3u) : 0u) | (in1 && id1 < 0 ? 2u : 0u);
-        bad |= lost << (2 * to);
+        odd |= (lost ? 1u : 0u) << to;
         if (lane == 0) {
+          ws.lost = (ws.lost & ~(3u << (2 * to))) | lost << (2 * to);
           if (lost) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
           const bool two = unit_shift && id1 >= 0;
           mbar_arrive_expect_tx(fb, 2 * rec * ((id0 >= 0 ? 1 : 0) + (two ? 1 : 0)));
@@ -475,7 +510,6 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           }
         }
       }
-      ++flying;
       ++pu;
     };
 #pragma unroll 1
@@ -483,15 +517,12 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 
     int stage = 0;
     uint32_t phase = 0;
-    long long pos = u0;
-    bool dead = false;
+    bool dead = false, more = true;
     // ---- items of the range
-    while (pos < u1) {
+    while (more) {
       const Walk w = ws.c;
-      const long long base = ws.cbase;
-      const int first = static_cast<int>(pos - base);
-      const long long item_end = base + w.seq.units;
-      const int last = static_cast<int>(min(static_cast<long long>(w.live), u1 - base));
+      const int first = static_cast<int>(max(ws.u0 - ws.cbase, 0ll));
+      const int last = static_cast<int>(min(static_cast<long long>(w.live), ws.u1 - ws.cbase));
       const int row0 = w.rg * p.rows_per_item;
       const int rows = min(p.rows_per_item, w.seq.qlen - row0);
       const int see0 = w.seq.ctx - w.seq.qlen + row0 + 1;  // keys the item's first row sees
@@ -531,16 +562,17 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         fac[nt][1] = __shfl_sync(FULL_MASK, f, 8 * qd + 4);
       }
       // the constant part of each chunk's scores: -1032 or -72 times q, summed
-      float cst[NC][NT][4];
+      float cst[NC][NT][2];
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float (&d)[4] = cst[c][nt];
-          d[0] = d[1] = d[2] = d[3] = 0.f;
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 2 * c; k < 2 * c + 2; ++k)
             mma_f16_16816(d, I4_NEG_EVEN, I4_NEG_EVEN, I4_NEG_ODD, I4_NEG_ODD, qf[k][nt][0], qf[k][nt][1]);
+          cst[c][nt][0] = d[0];
+          cst[c][nt][1] = d[1];
         }
       float o[2 * NC][NT][4];
       float l[NT][2], m[NT][2];
@@ -580,13 +612,14 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
               const float f0 = half_of(sc0[cp], x), f1 = half_of(sc1[cp], x);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                float d[4];
-                mma_f16_from(d, a[0], b[0], a[1], b[1], qf[2 * c][nt][0], qf[2 * c][nt][1], cst[c][nt]);
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16_16816(d, a[0], b[0], a[1], b[1], qf[2 * c][nt][0], qf[2 * c][nt][1]);
                 mma_f16_16816(d, a[2], b[2], a[3], b[3], qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const float f = i < 2 ? f0 : f1;
-                  y[mt][nt][i] = c == 0 ? d[i] * f : fmaf(d[i], f, y[mt][nt][i]);
+                  const float x = d[i] + cst[c][nt][i & 1];
+                  y[mt][nt][i] = c == 0 ? x * f : fmaf(x, f, y[mt][nt][i]);
                 }
               }
             }
@@ -715,15 +748,13 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll 1
       for (int u = first; u < last; ++u) {
         const uint32_t ka = ring_at + stage * C::STAGE_BYTES;
-        const unsigned lost = (bad >> (2 * stage)) & 3u;
         if (!__all_sync(FULL_MASK, !dead && mbar_wait(bar + stage, phase))) {
           dead = true;
           break;
         }
-        --flying;
         // (some key is masked for some column, or none is: two copies of the body)
-        if (u * I4_UNIT + I4_UNIT > see0 || lost)
-          unit(std::true_type{}, u, ka, lost);
+        if (u * I4_UNIT + I4_UNIT > see0 || (odd >> stage & 1))
+          unit(std::true_type{}, u, ka, ws.lost >> (2 * stage) & (odd >> stage & 1 ? 3u : 0u));
         else
           unit(std::false_type{}, u, ka, 0u);
         __syncwarp();  // every lane has read the stage
@@ -734,7 +765,9 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         }
       }
       // ---- the item's end, or the range's
-      const bool starts = pos == base, finishes = item_end <= u1;
+      const long long base = ws.cbase, item_end = base + ws.c.seq.units, end = ws.u1;
+      const bool starts = base >= ws.u0, finishes = item_end <= end;
+      const int row = ws.c.seq.q0 + ws.c.rg * p.rows_per_item, h = ws.c.h;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -742,13 +775,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll
           for (int x = 4; x <= 16; x <<= 1) l[nt][j] += __shfl_xor_sync(FULL_MASK, l[nt][j], x);
       if (starts && finishes) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
-          __nv_bfloat16* dst = out_place(w.seq.q0 + row0, w.h, nt);
-#pragma unroll
-          for (int k = 0; k < 2 * NC; ++k) store_tile(dst + k * 16, o[k][nt], i0, i1, rowB(nt) < rows);
-        }
+        write_out(o, l, row, rows, h);
       } else {
         const int slot = starts ? 1 : 0;
         float4* rec_out = reinterpret_cast<float4*>(piece0 + slot * C::PIECE) + lane;
@@ -759,13 +786,100 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
             rec_out[(k * NT + nt) * 32] = make_float4(o[k][nt][0], o[k][nt][1], o[k][nt][2], o[k][nt][3]);
           rec_out[(2 * NC * NT + nt) * 32] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
         }
-        WarpEnd& we = ends[warp];
-        if (lane == 0) {
-          we.row[slot] = w.seq.q0 + row0;
+        // Merged at once, by the warp that brings the last piece: an item inside the CTA, and one that few warps of
+        // several CTAs share.  Where not every warp has a unit, none has more than one: a piece per unit.
+        const bool local = base >= c0 && item_end <= c0 + cn;
+        const int w0 = warp_of(base);
+        const int n = dense ? warp_of(item_end - 1) - w0 + 1 : static_cast<int>(item_end - base);
+        const int self = dense ? static_cast<int>(blockIdx.x) * WARPS + warp - w0 : static_cast<int>(ws.u0 - base);
+        if (local || n <= I4_FEW) {
+          int got = 0;
+          if (local) {
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) got = atomicAdd(&arrived[w0 - blockIdx.x * WARPS], 1);
+            got = __shfl_sync(FULL_MASK, got, 0);
+            __threadfence_block();
+          } else {
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) {
+              got = atomicAdd(p.counters + I4_WARP_COUNTERS + w0, 1);
+              if (got == n - 1) p.counters[I4_WARP_COUNTERS + w0] = 0;
+            }
+            got = __shfl_sync(FULL_MASK, got, 0);
+            __threadfence();
+          }
+          if (got == n - 1) {
+            const auto piece = [&](int i) {
+              const int at = dense ? w0 + i : warp_of(base + i);
+              return reinterpret_cast<const float4*>(p.warp_pieces +
+                                                     (static_cast<long long>(at) * 2 + (i == 0 ? 1 : 0)) * C::PIECE) + lane;
+            };
+            float top[NT][2], sum[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                top[nt][j] = l[nt][j] != 0.f ? m[nt][j] : I4_NO_MAX;
+                sum[nt][j] = 0.f;
+              }
+#pragma unroll 2
+            for (int i = 0; i < n; ++i) {
+              if (i == self) continue;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float4 ml = __ldcg(piece(i) + (2 * NC * NT + nt) * 32);
+                if (ml.z != 0.f) top[nt][0] = fmaxf(top[nt][0], ml.x);
+                if (ml.w != 0.f) top[nt][1] = fmaxf(top[nt][1], ml.y);
+              }
+            }
+            float acc[2 * NC][NT][4];
+#pragma unroll
+            for (int k = 0; k < 2 * NC; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[k][nt][x] = 0.f;
+            for (int i = 0; i < n; ++i) {  // in the pieces' order, whoever merges
+              const float4* r = piece(i);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float4 ml = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
+                if (i != self) ml = __ldcg(r + (2 * NC * NT + nt) * 32);
+                const float a = ml.z != 0.f ? fast_exp2(ml.x - top[nt][0]) : 0.f;
+                const float b = ml.w != 0.f ? fast_exp2(ml.y - top[nt][1]) : 0.f;
+                sum[nt][0] += ml.z * a;
+                sum[nt][1] += ml.w * b;
+                if (i == self) {
+#pragma unroll
+                  for (int k = 0; k < 2 * NC; ++k) {
+                    acc[k][nt][0] += o[k][nt][0] * a;
+                    acc[k][nt][1] += o[k][nt][1] * b;
+                    acc[k][nt][2] += o[k][nt][2] * a;
+                    acc[k][nt][3] += o[k][nt][3] * b;
+                  }
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 2 * NC; ++k) {
+                    const float4 x = __ldcg(r + (k * NT + nt) * 32);
+                    acc[k][nt][0] += x.x * a;
+                    acc[k][nt][1] += x.y * b;
+                    acc[k][nt][2] += x.z * a;
+                    acc[k][nt][3] += x.w * b;
+                  }
+                }
+              }
+            }
+            write_out(acc, sum, row, rows, h);
+          }
+        } else if (lane == 0) {
+          WarpEnd& we = ends[warp];
+          we.row[slot] = row;
           we.rows[slot] = rows;
-          we.h[slot] = w.h;
+          we.h[slot] = h;
           we.first[slot] = base;
-          we.units[slot] = w.seq.units;
+          we.units[slot] = ws.c.seq.units;
           if (slot == 0) {
             we.has0 = 1;
             we.on0 = !finishes;
@@ -774,8 +888,8 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           }
         }
       }
-      pos = min(item_end, u1);
-      if (pos < u1) {
+      more = item_end < end;
+      if (more) {
         __syncwarp();
         if (lane == 0) {
           ws.cbase = item_end;
@@ -786,7 +900,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
     }
     if (dead) {  // a copy did not land in time: report it, and give those in flight as long again
       if (lane == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_TIMEOUT));
-      for (; flying > 0; --flying) {
+      for (int i = 0; i < STAGES; ++i) {
         (void)mbar_wait(bar + stage, phase);
         if (++stage == STAGES) {
           stage = 0;
@@ -797,19 +911,16 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   }
   __syncthreads();
 
+  // ---- what is left: items that many warps of several CTAs share
+  bool any = false;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) any |= ends[w].has0 || ends[w].has1;
+  if (!any) return;
+
   // ---- merge the CTA's pieces.  Chain e: the item the CTA's range starts inside
   // of (e = 0), or the one that starts in warp e - 1 and goes on past it.
   float* cta_piece = p.cta_pieces + static_cast<long long>(blockIdx.x) * 2 * C::PIECE;
   const float* pieces = p.warp_pieces + static_cast<long long>(blockIdx.x) * WARPS * 2 * C::PIECE;
-  const auto finish = [&](const float (&o)[2][NT][4], const float (&l)[NT][2], int k, int row, int rows, int h) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
-      __nv_bfloat16* dst = out_place(row, h, nt) + k * 32;
-      store_tile(dst, o[0][nt], i0, i1, rowB(nt) < rows);
-      store_tile(dst + 16, o[1][nt], i0, i1, rowB(nt) < rows);
-    }
-  };
   int job = 0;
   for (int e = 0; e <= WARPS; ++e) {
     if (e == 0 ? !ends[0].has0 : !ends[e - 1].has1) continue;
@@ -882,7 +993,6 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   }
 }
 
-constexpr size_t I4_COUNTER_BYTES = 4096;  // one int per CTA
 
 template <int D, int NT>
 size_t workspace_of(int num_sms) {
@@ -948,7 +1058,7 @@ int run_int4(void* out, const void* q, const int32_t* query_start, const void* k
   DeviceInfo di;
   const int rc = device_info(&di);
   if (rc != PA_OK) return rc;
-  if (di.num_sms * static_cast<int>(sizeof(int)) > static_cast<int>(I4_COUNTER_BYTES)) return PA_ERR_UNSUPPORTED;
+  if (di.num_sms > I4_WARP_COUNTERS) return PA_ERR_UNSUPPORTED;
   if (workspace_bytes < int4_workspace(head_dim, di.num_sms)) return PA_ERR_WORKSPACE;
   Int4Params p{};
   p.out = static_cast<__nv_bfloat16*>(out);
