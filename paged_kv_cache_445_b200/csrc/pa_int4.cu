@@ -44,27 +44,24 @@ namespace pa {
 
 namespace {
 
-#ifndef I4_W
-#define I4_W 12
-#endif
-constexpr int I4_UNIT = 32;        // keys
 constexpr int I4_FEW = 6;             // pieces of an item across CTAs that one warp merges
 constexpr int I4_WARP_COUNTERS = 512; // counters: per CTA, then (from here) per warp
 constexpr size_t I4_COUNTER_BYTES = 4 * (512 + 512 * 16);
-#ifndef I4_PAD
-#define I4_PAD 1
-#endif
+constexpr int I4_PAD = 1;              // units that starting and ending an item costs
+constexpr int I4_FOLD = 8;             // units between two corrections of O
 constexpr float I4_NO_MAX = -3e38f; // maximum over no pieces
 
 template <int D, int NT>
 struct I4 {
   static constexpr int NC = D / 32;                         // chunks of a row
   static constexpr int COLS = 8 * NT;
-  static constexpr int WARPS = D * NT <= 128 ? I4_W : 8;      // 128 or 255 registers a thread
+  static constexpr int WARPS = 8;
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int PER = WARPS > 8 ? 1 : 2;            // prefix sums of the batch's units, per thread
+  static constexpr int PER = 2;                             // prefix sums of the batch's units, per thread
   static constexpr int BUCKETS = THREADS * PER;            // of runs of sequences
-  static constexpr int HALF_BYTES = I4_UNIT * (D * 9 / 16); // K (or V) of a unit
+  static constexpr int MT = D * NT >= 256 ? 2 : 4;          // 16-key m-tiles of a unit: what the registers hold
+  static constexpr int UNIT = 16 * MT;
+  static constexpr int HALF_BYTES = UNIT * (D * 9 / 16);    // K (or V) of a unit
   static constexpr int STAGE_BYTES = 2 * HALF_BYTES;
   static constexpr int STAGES = 221184 / WARPS / STAGE_BYTES;
   // a piece, in floats, as the lanes hold it: O [2 NC][NT] and (m, m, l, l) [NT] of 32 lanes x 4
@@ -93,7 +90,7 @@ struct SeqInfo {
   int q0, qlen, ctx, units;  // units of one item (0: no work), from the whole context
 };
 
-__device__ __forceinline__ SeqInfo i4_seq(const Int4Params& p, int s, int* bits = nullptr) {
+__device__ __forceinline__ SeqInfo i4_seq(const Int4Params& p, int s, int unit, int* bits = nullptr) {
   SeqInfo i;
   i.ctx = p.context_lens[s];
   i.q0 = s;
@@ -114,7 +111,7 @@ __device__ __forceinline__ SeqInfo i4_seq(const Int4Params& p, int s, int* bits 
     bad = PA_STATUS_BIT(PA_ERR_RANGE);
     i.ctx = 0;
   }
-  i.units = i.ctx > 0 && i.qlen > 0 ? (i.ctx + I4_UNIT - 1) / I4_UNIT + I4_PAD : 0;
+  i.units = i.ctx > 0 && i.qlen > 0 ? (i.ctx + unit - 1) / unit + I4_PAD : 0;
   if (bits) *bits |= bad;
   return i;
 }
@@ -131,24 +128,24 @@ struct Walk {
   int live;  // units of the item that some row sees
 };
 
-__device__ __forceinline__ void i4_enter(const Int4Params& p, Walk& w) {
+__device__ __forceinline__ void i4_enter(const Int4Params& p, Walk& w, int unit) {
   const int last = min((w.rg + 1) * p.rows_per_item, w.seq.qlen);  // rows of the item end here
   const int keys = w.seq.ctx - w.seq.qlen + last;
-  w.live = keys > 0 ? (keys + I4_UNIT - 1) / I4_UNIT : 0;
+  w.live = keys > 0 ? (keys + unit - 1) / unit : 0;
 }
 
-__device__ __forceinline__ void i4_next(const Int4Params& p, Walk& w) {
+__device__ __forceinline__ void i4_next(const Int4Params& p, Walk& w, int unit) {
   if (++w.h == p.num_kv_heads) {
     w.h = 0;
     if (++w.rg == w.groups) {
       w.rg = 0;
       do {
         if (++w.s >= p.num_seqs) return;  // the range ends before this is used
-        w.seq = i4_seq(p, w.s);
+        w.seq = i4_seq(p, w.s, unit);
       } while (w.seq.units == 0);
       w.groups = i4_groups(p, w.seq.qlen);
     }
-    i4_enter(p, w);
+    i4_enter(p, w, unit);
   }
 }
 
@@ -158,30 +155,22 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// 8 codes (nibbles of the two halves of w) -> 4 fp16 pairs: 1024 + u in 0 and 2, 64 + u in 1 and 3 (the nibble
-// lies in the mantissa where its lowest bit is worth one: five operations).
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
-  return d;
-}
-// The two masks and the two exponents, in registers: an instruction holds one constant of its own, no more.
-struct Magic {
-  uint32_t even, odd;
-};
-__device__ __forceinline__ void i4_expand(uint32_t w, const Magic& e, uint32_t (&h)[4]) {
+// 8 codes (nibbles of the two halves of w) -> 4 fp16 pairs.  A nibble left alone in the mantissa is the subnormal
+// number u 2^-24 (0 and 2) or u 2^-20 (1 and 3): nothing to convert, five operations.
+__device__ __forceinline__ void i4_expand(uint32_t w, uint32_t (&h)[4]) {
   const uint32_t b = w >> 8;
-  h[0] = and_or(w, 0x000f000fu, e.even);
-  h[1] = and_or(w, 0x00f000f0u, e.odd);
-  h[2] = and_or(b, 0x000f000fu, e.even);
-  h[3] = and_or(b, 0x00f000f0u, e.odd);
+  h[0] = w & 0x000f000fu;
+  h[1] = w & 0x00f000f0u;
+  h[2] = b & 0x000f000fu;
+  h[3] = b & 0x00f000f0u;
 }
-constexpr uint32_t I4_OFF_EVEN = 0x64086408u, I4_OFF_ODD = 0x54805480u;    // 1024 + 8, 64 + 8
-constexpr uint32_t I4_NEG_EVEN = 0xe408e408u, I4_NEG_ODD = 0xd480d480u;
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+constexpr uint32_t I4_NEG8_EVEN = 0x80088008u, I4_NEG8_ODD = 0x80808080u;  // -8 in the two places
+// D[16x8] += A[16x8] B[8x8]
+__device__ __forceinline__ void mma_f16_1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -267,14 +256,14 @@ struct WarpState {
   Walk c, p;               // consumer's and producer's place
   long long cbase, pbase;  // first units of their items
   long long u0, u1;        // the warp's range
-  unsigned lost;           // two bits per stage: blocks of its unit that were not loaded
+  unsigned lost[8];        // per stage: m-tiles of its unit that were not loaded
 };
 
 // VARLEN: several query rows per sequence (columns see different numbers of keys).
 template <int D, int NT, bool VARLEN>
 __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __grid_constant__ Int4Params p) {
   using C = I4<D, NT>;
-  constexpr int NC = C::NC, WARPS = C::WARPS, STAGES = C::STAGES;
+  constexpr int NC = C::NC, WARPS = C::WARPS, STAGES = C::STAGES, MT = C::MT, UNIT = C::UNIT;
   extern __shared__ __align__(128) uint8_t smem[];
   long long* prefix = reinterpret_cast<long long*>(smem + C::RING_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES + 8 * C::BUCKETS);
@@ -295,9 +284,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   }
 
   grid_dependency_wait();
-#ifndef NOPDL
-  grid_launch_dependents();
-#endif
+  grid_launch_dependents();  // the next kernel's launch overlaps this one; it waits for this one's end itself
 
   // ---- units of the batch: prefix sums over runs of sequences
   const int run = (p.num_seqs + C::BUCKETS - 1) / C::BUCKETS;
@@ -308,7 +295,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   for (int i = 0; i < PER; ++i) {
     const int b = tid * PER + i;
     for (int s = b * run; s < min((b + 1) * run, p.num_seqs); ++s) {
-      const SeqInfo q = i4_seq(p, s, &bits);
+      const SeqInfo q = i4_seq(p, s, UNIT, &bits);
       sum += static_cast<long long>(q.units) * i4_groups(p, q.qlen) * p.num_kv_heads;
     }
     mine[i] = sum;
@@ -335,7 +322,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   // rows without a key
   const int row_vecs = p.num_q_heads * D / 8;
   for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
-    const SeqInfo q = i4_seq(p, s);
+    const SeqInfo q = i4_seq(p, s, UNIT);
     if (q.units == 0 && q.qlen > 0) {
       uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<long long>(q.q0) * p.num_q_heads * D);
       for (long long i = tid; i < static_cast<long long>(q.qlen) * row_vecs; i += C::THREADS)
@@ -398,10 +385,9 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   const uint32_t ring_at = smem_u32(smem) + warp * STAGES * C::STAGE_BYTES;
   uint64_t* bar = bars + warp * STAGES;
   const int rec = int4_record_bytes(bs, D);
-  const int unit_shift = 5 - p.block_shift;  // log2 of the blocks of a unit
+  const int half_unit = p.block_shift - 4;  // 1: a block holds two m-tiles
+  const int blocks = MT >> half_unit;       // of a unit
   WarpState& ws = walks[warp];
-  Magic magic{0x64006400u, 0x54005400u};
-  asm volatile("" : "+r"(magic.even), "+r"(magic.odd));
 
   if (u0 < u1) {
     // ---- find the item of u0
@@ -415,7 +401,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       Walk w;
       int s = lo * run;
       for (;; ++s) {
-        w.seq = i4_seq(p, s);
+        w.seq = i4_seq(p, s, UNIT);
         w.groups = i4_groups(p, w.seq.qlen);
         const long long n = static_cast<long long>(w.seq.units) * w.groups * p.num_kv_heads;
         if (at + n > u0) break;
@@ -425,13 +411,12 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       w.s = s;
       w.rg = static_cast<int>(item / p.num_kv_heads);
       w.h = static_cast<int>(item - static_cast<long long>(w.rg) * p.num_kv_heads);
-      i4_enter(p, w);
+      i4_enter(p, w, UNIT);
       if (lane == 0) {
         ws.c = ws.p = w;
         ws.cbase = ws.pbase = at + item * w.seq.units;
         ws.u0 = u0;
         ws.u1 = u1;
-        ws.lost = 0;
       }
       __syncwarp();
     }
@@ -454,7 +439,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           __syncwarp();
           if (lane == 0) {
             ws.pbase = next;
-            i4_next(p, ws.p);
+            i4_next(p, ws.p, UNIT);
           }
           __syncwarp();
           pu = 0;
@@ -464,7 +449,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         head_off = ws.p.h * rec;
         ids_from = INT32_MAX;
       }
-      const int entry = pu << unit_shift;
+      const int entry = pu * blocks;
       if (static_cast<unsigned>(entry - ids_from) >= 32u) {
         ids_from = entry;
         ids = entry + lane < entries
@@ -472,42 +457,46 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
                   : -1;
         if (ids >= p.num_blocks) ids = -1;
       }
-      const int id0 = __shfl_sync(FULL_MASK, ids, entry - ids_from);
-      const int id1 = __shfl_sync(FULL_MASK, ids, entry + unit_shift - ids_from);  // bs 32: the same again
+      int id[MT], all = 0;  // (blocks of 32: every other one)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        id[i] = __shfl_sync(FULL_MASK, ids, entry - ids_from + (i >> half_unit));
+        all |= id[i];
+      }
       const uint32_t dst = ring_at + to * C::STAGE_BYTES;
       uint64_t* fb = bar + to;
       odd &= ~(1u << to);
-      if ((id0 | id1) >= 0) {
+      if (all >= 0) {
         if (lane == 0) {
           mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
-          const uint8_t* k0 = p.k_cache + static_cast<unsigned long long>(id0) * stride + head_off;
-          bulk_load(dst, k0, rec, fb);
-          bulk_load(dst + C::HALF_BYTES, k0 + k_to_v, rec, fb);
-          if (unit_shift) {
-            const uint8_t* k1 = p.k_cache + static_cast<unsigned long long>(id1) * stride + head_off;
-            bulk_load(dst + rec, k1, rec, fb);
-            bulk_load(dst + C::HALF_BYTES + rec, k1 + k_to_v, rec, fb);
-          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            if (!(half_unit && (i & 1))) {
+              const uint8_t* k = p.k_cache + static_cast<unsigned long long>(id[i]) * stride + head_off;
+              bulk_load(dst + (i >> half_unit) * rec, k, rec, fb);
+              bulk_load(dst + C::HALF_BYTES + (i >> half_unit) * rec, k + k_to_v, rec, fb);
+            }
         }
-      } else {  // the last block of a context, or a bad ID
-        const bool in1 = unit_shift && entry + 1 < entries;
-        const unsigned lost = (id0 < 0 ? (unit_shift ? 1u : 3u) : 0u) | (in1 && id1 < 0 ? 2u : 0u);
+      } else {  // the last blocks of a context, or a bad ID
+        unsigned lost = 0;  // by m-tile
+        int there = 0;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          if (id[i] < 0 && entry + (i >> half_unit) < entries) lost |= 1u << i;
+          if (id[i] >= 0 && !(half_unit && (i & 1))) ++there;
+        }
         odd |= (lost ? 1u : 0u) << to;
         if (lane == 0) {
-          ws.lost = (ws.lost & ~(3u << (2 * to))) | lost << (2 * to);
+          ws.lost[to] = lost;
           if (lost) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
-          const bool two = unit_shift && id1 >= 0;
-          mbar_arrive_expect_tx(fb, 2 * rec * ((id0 >= 0 ? 1 : 0) + (two ? 1 : 0)));
-          if (id0 >= 0) {
-            const uint8_t* k0 = p.k_cache + static_cast<unsigned long long>(id0) * stride + head_off;
-            bulk_load(dst, k0, rec, fb);
-            bulk_load(dst + C::HALF_BYTES, k0 + k_to_v, rec, fb);
-          }
-          if (two) {
-            const uint8_t* k1 = p.k_cache + static_cast<unsigned long long>(id1) * stride + head_off;
-            bulk_load(dst + rec, k1, rec, fb);
-            bulk_load(dst + C::HALF_BYTES + rec, k1 + k_to_v, rec, fb);
-          }
+          mbar_arrive_expect_tx(fb, 2 * rec * there);
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            if (id[i] >= 0 && !(half_unit && (i & 1))) {
+              const uint8_t* k = p.k_cache + static_cast<unsigned long long>(id[i]) * stride + head_off;
+              bulk_load(dst + (i >> half_unit) * rec, k, rec, fb);
+              bulk_load(dst + C::HALF_BYTES + (i >> half_unit) * rec, k + k_to_v, rec, fb);
+            }
         }
       }
       ++pu;
@@ -555,33 +544,51 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         for (int k = 0; k < 2 * NC; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            qf[k][nt][i] = pack_f16x2(__uint_as_float(raw[k][i] << 16) * down,
-                                      __uint_as_float(raw[k][i] & 0xffff0000u) * down);
-        const float f = ldexpf(p.scale_log2, e);
+            qf[k][nt][i] = pack_f16x2(__uint_as_float(raw[k][i] << 16) * down * (i ? 1024.f : 16384.f),
+                                      __uint_as_float(raw[k][i] & 0xffff0000u) * down * (i ? 1024.f : 16384.f));
+        const float f = ldexpf(p.scale_log2, e + 10);
         fac[nt][0] = __shfl_sync(FULL_MASK, f, 8 * qd);  // column 2 qd lives in lanes 4 (2 qd) ..
         fac[nt][1] = __shfl_sync(FULL_MASK, f, 8 * qd + 4);
       }
-      // the constant part of each chunk's scores: -1032 or -72 times q, summed
-      float cst[NC][NT][2];
+      // The codes carry 8 too many: -8 sum(q) of every chunk, as the B operand of one more product with the chunks'
+      // scales (k: the chunks' high parts, then their low parts).
+      uint32_t qc[NT][2];
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t hi[NC / 2], lo[NC / 2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < NC; c += 2) {
+          float x[2];
 #pragma unroll
-          for (int k = 2 * c; k < 2 * c + 2; ++k)
-            mma_f16_16816(d, I4_NEG_EVEN, I4_NEG_EVEN, I4_NEG_ODD, I4_NEG_ODD, qf[k][nt][0], qf[k][nt][1]);
-          cst[c][nt][0] = d[0];
-          cst[c][nt][1] = d[1];
+          for (int i = 0; i < 2; ++i) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 2 * (c + i); k < 2 * (c + i) + 2; ++k)
+              mma_f16_16816(d, I4_NEG8_EVEN, I4_NEG8_EVEN, I4_NEG8_ODD, I4_NEG8_ODD, qf[k][nt][0], qf[k][nt][1]);
+            const float e0 = __shfl_sync(FULL_MASK, d[0], g >> 1), e1 = __shfl_sync(FULL_MASK, d[1], g >> 1);
+            x[i] = g & 1 ? e1 : e0;  // of column g
+          }
+          hi[c / 2] = pack_f16x2(x[0], x[1]);
+          lo[c / 2] = pack_f16x2(x[0] - half_of(hi[c / 2], 0), x[1] - half_of(hi[c / 2], 1));
         }
+        if constexpr (NC == 2) {
+          qc[nt][0] = qd == 0 ? hi[0] : qd == 1 ? lo[0] : 0u;
+        } else if constexpr (NC == 4) {
+          qc[nt][0] = qd == 0 ? hi[0] : qd == 1 ? hi[1] : qd == 2 ? lo[0] : lo[1];
+        } else {
+          qc[nt][0] = qd == 0 ? hi[0] : qd == 1 ? hi[1] : qd == 2 ? hi[2] : hi[3];
+          qc[nt][1] = qd == 0 ? lo[0] : qd == 1 ? lo[1] : qd == 2 ? lo[2] : lo[3];
+        }
+      }
       float o[2 * NC][NT][4];
+      float over[NC][NT][4];  // -8 times the weights' sum, per chunk: what the codes' 8 adds to O
       float l[NT][2], m[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int k = 0; k < 2 * NC; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[k][nt][i] = 0.f;
+          for (int i = 0; i < 4; ++i) o[k][nt][i] = over[k / 2][nt][i] = 0.f;
         l[nt][0] = l[nt][1] = 0.f;
         m[nt][0] = m[nt][1] = 0.f;
       }
@@ -590,15 +597,38 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
       const auto unit = [&](auto partial, int u, uint32_t ka, unsigned lost) {
         constexpr bool PARTIAL = decltype(partial)::value;
 
-        // ---- scores of 32 keys
-        float y[2][NT][4];
+        // where m-tile mt's codes and scales stand (within K or V)
+        const auto codes_at = [&](int mt) {
+          return half_unit ? (mt >> 1) * rec + (mt & 1) * 16 * (D / 2) : mt * rec;
+        };
+        const auto scales_at = [&](int mt) {
+          return half_unit ? (mt >> 1) * rec + 32 * (D / 2) + (mt & 1) * 16 * 2 * NC : mt * rec + 16 * (D / 2);
+        };
+        const int seen = see0 + rows - 1 - u * UNIT;  // keys of the unit that some column sees
+        // ---- scores
+        float y[MT][NT][4];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t rb = ka + (bs == 16 ? mt * rec : mt * 16 * (D / 2));
-          const uint32_t sb = ka + (bs == 16 ? mt * rec + 16 * (D / 2) : 32 * (D / 2) + mt * 16 * (2 * NC));
+        for (int mt = 0; mt < MT; ++mt) {
+          if (PARTIAL && mt * 16 >= seen) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) y[mt][nt][0] = y[mt][nt][1] = y[mt][nt][2] = y[mt][nt][3] = 0.f;
+            continue;
+          }
+          const uint32_t rb = ka + codes_at(mt), sb = ka + scales_at(mt);
           uint32_t sc0[NC / 2], sc1[NC / 2];
           lds_words(sb + g * 2 * NC, sc0);
           lds_words(sb + (g + 8) * 2 * NC, sc1);
+          uint32_t wa[1], wb[1];
+          lds_words(sb + g * 2 * NC + (qd * 4 & (2 * NC - 1)), wa);
+          lds_words(sb + (g + 8) * 2 * NC + (qd * 4 & (2 * NC - 1)), wb);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            y[mt][nt][0] = y[mt][nt][1] = y[mt][nt][2] = y[mt][nt][3] = 0.f;
+            if constexpr (NC == 8)
+              mma_f16_16816(y[mt][nt], wa[0], wb[0], wa[0], wb[0], qc[nt][0], qc[nt][1]);
+            else
+              mma_f16_1688(y[mt][nt], wa[0], wb[0], qc[nt][0]);
+          }
 #pragma unroll
           for (int cp = 0; cp < NC / 2; ++cp) {
             uint32_t r[4];
@@ -607,8 +637,8 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
             for (int x = 0; x < 2; ++x) {  // chunk 2 cp + x: rows 0-7 in r[2 x], rows 8-15 in r[2 x + 1]
               const int c = 2 * cp + x;
               uint32_t a[4], b[4];
-              i4_expand(r[2 * x], magic, a);
-              i4_expand(r[2 * x + 1], magic, b);
+              i4_expand(r[2 * x], a);
+              i4_expand(r[2 * x + 1], b);
               const float f0 = half_of(sc0[cp], x), f1 = half_of(sc1[cp], x);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
@@ -616,11 +646,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
                 mma_f16_16816(d, a[0], b[0], a[1], b[1], qf[2 * c][nt][0], qf[2 * c][nt][1]);
                 mma_f16_16816(d, a[2], b[2], a[3], b[3], qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float f = i < 2 ? f0 : f1;
-                  const float x = d[i] + cst[c][nt][i & 1];
-                  y[mt][nt][i] = c == 0 ? x * f : fmaf(x, f, y[mt][nt][i]);
-                }
+                for (int i = 0; i < 4; ++i) y[mt][nt][i] = fmaf(d[i], i < 2 ? f0 : f1, y[mt][nt][i]);
               }
             }
           }
@@ -630,7 +656,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               y[mt][nt][i] = fmaf(y[mt][nt][i], fac[nt][i & 1], -m[nt][i & 1]);
@@ -640,11 +666,11 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int row = rowA(nt, i & 1);
-                if (u * I4_UNIT + mt * 16 + (i >> 1) * 8 + g >= (row < rows ? see0 + row : 0) || (lost >> mt & 1))
+                if (u * UNIT + mt * 16 + (i >> 1) * 8 + g >= (row < rows ? see0 + row : 0) || (lost >> mt & 1))
                   y[mt][nt][i] = -INFINITY;
                 top = fmaxf(top, y[mt][nt][i]);
               }
@@ -654,7 +680,9 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float mx = fmaxf(fmaxf(y[0][nt][j], y[0][nt][j + 2]), fmaxf(y[1][nt][j], y[1][nt][j + 2]));
+              float mx = fmaxf(y[0][nt][j], y[0][nt][j + 2]);
+#pragma unroll
+              for (int mt = 1; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(y[mt][nt][j], y[mt][nt][j + 2]));
               mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 16));
@@ -665,7 +693,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
               m[nt][j] = m[nt][j] + up;
               l[nt][j] *= a;
 #pragma unroll
-              for (int mt = 0; mt < 2; ++mt) {
+              for (int mt = 0; mt < MT; ++mt) {
                 y[mt][nt][j] -= up;
                 y[mt][nt][j + 2] -= up;
               }
@@ -674,13 +702,18 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
                 o[k][nt][j] *= a;
                 o[k][nt][j + 2] *= a;
               }
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+                over[c][nt][j] *= a;
+                over[c][nt][j + 2] *= a;
+              }
             }
         }
-        uint32_t pf[2][NT][2];  // B operand: keys 2 qd, 2 qd + 1 (and + 8) of column g
+        uint32_t pf[MT][NT][2];  // B operand: keys 2 qd, 2 qd + 1 (and + 8) of column g
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
+          for (int mt = 0; mt < MT; ++mt) {
             float e[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -691,18 +724,18 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
             pf[mt][nt][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
           }
         // ---- values
+        const uint32_t va = ka + C::HALF_BYTES;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t va = ka + C::HALF_BYTES;
-          const uint32_t rb = va + (bs == 16 ? mt * rec : mt * 16 * (D / 2));
-          const uint32_t sb = va + (bs == 16 ? mt * rec + 16 * (D / 2) : 32 * (D / 2) + mt * 16 * (2 * NC));
+        for (int mt = 0; mt < MT; ++mt) {
+          if (PARTIAL && mt * 16 >= seen) continue;
+          const uint32_t rb = va + codes_at(mt), sb = va + scales_at(mt);
           uint32_t w0[NC / 2], w1[NC / 2], w2[NC / 2], w3[NC / 2];
           lds_words(sb + (2 * qd) * 2 * NC, w0);
           lds_words(sb + (2 * qd + 1) * 2 * NC, w1);
           lds_words(sb + (2 * qd + 8) * 2 * NC, w2);
           lds_words(sb + (2 * qd + 9) * 2 * NC, w3);
           if (PARTIAL) {  // the scale of a key that no column sees may be anything: zero times it must stay zero
-            const int k0 = u * I4_UNIT + mt * 16 + 2 * qd, lim = (lost >> mt & 1) ? 0 : see0 + rows - 1;
+            const int k0 = mt * 16 + 2 * qd, lim = (lost >> mt & 1) ? 0 : seen;
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) {
               if (k0 >= lim) w0[i] = 0;
@@ -719,24 +752,20 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
             for (int x = 0; x < 2; ++x) {  // chunk 2 cp + x: keys 0-7 in r[2 x], keys 8-15 in r[2 x + 1]
               const int c = 2 * cp + x;
               uint32_t a[4], b[4];
-              i4_expand(r[2 * x], magic, a);
-              i4_expand(r[2 * x + 1], magic, b);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a[i] = hsub2(a[i], i & 1 ? I4_OFF_ODD : I4_OFF_EVEN);
-                b[i] = hsub2(b[i], i & 1 ? I4_OFF_ODD : I4_OFF_EVEN);
-              }
+              i4_expand(r[2 * x], a);
+              i4_expand(r[2 * x + 1], b);
               const uint32_t s01 = __byte_perm(w0[cp], w1[cp], x ? 0x7632 : 0x5410);
               const uint32_t s89 = __byte_perm(w2[cp], w3[cp], x ? 0x7632 : 0x5410);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 uint32_t b0 = hmul2(pf[mt][nt][0], s01), b1 = hmul2(pf[mt][nt][1], s89);
                 if (VARLEN && PARTIAL) {  // likewise the scale of a key that this column does not see
-                  const int k0 = u * I4_UNIT + mt * 16 + 2 * qd;
+                  const int k0 = u * UNIT + mt * 16 + 2 * qd;
                   const int lim = (lost >> mt) & 1 ? 0 : see0 + rowB(nt);
                   b0 &= (k0 < lim ? 0xffffu : 0u) | (k0 + 1 < lim ? 0xffff0000u : 0u);
                   b1 &= (k0 + 8 < lim ? 0xffffu : 0u) | (k0 + 9 < lim ? 0xffff0000u : 0u);
                 }
+                mma_f16_16816(over[c][nt], I4_NEG8_EVEN, I4_NEG8_ODD, I4_NEG8_EVEN, I4_NEG8_ODD, b0, b1);
                 mma_f16_16816(o[2 * c][nt], a[0], a[1], b[0], b[1], b0, b1);
                 mma_f16_16816(o[2 * c + 1][nt], a[2], a[3], b[2], b[3], b0, b1);
               }
@@ -745,6 +774,18 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         }
       };
 
+      const auto settle = [&]() {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[2 * c][nt][i] += over[c][nt][i];
+              o[2 * c + 1][nt][i] += over[c][nt][i];
+              over[c][nt][i] = 0.f;
+            }
+      };
 #pragma unroll 1
       for (int u = first; u < last; ++u) {
         const uint32_t ka = ring_at + stage * C::STAGE_BYTES;
@@ -753,17 +794,26 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
           break;
         }
         // (some key is masked for some column, or none is: two copies of the body)
-        if (u * I4_UNIT + I4_UNIT > see0 || (odd >> stage & 1))
-          unit(std::true_type{}, u, ka, ws.lost >> (2 * stage) & (odd >> stage & 1 ? 3u : 0u));
+        if (u * UNIT + UNIT > see0 || (odd >> stage & 1))
+          unit(std::true_type{}, u, ka, odd >> stage & 1 ? ws.lost[stage] : 0u);
         else
           unit(std::false_type{}, u, ka, 0u);
         __syncwarp();  // every lane has read the stage
         produce(stage);
+        // O holds sums of u, not of u - 8: taken off before they grow past what their last bits can tell
+        if ((u & (I4_FOLD - 1)) == I4_FOLD - 1) settle();
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
+      settle();
+#pragma unroll
+      for (int k = 0; k < 2 * NC; ++k)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[k][nt][i] *= i < 2 ? 16777216.f : 1048576.f;  // the codes' 2^-24 and 2^-20
       // ---- the item's end, or the range's
       const long long base = ws.cbase, item_end = base + ws.c.seq.units, end = ws.u1;
       const bool starts = base >= ws.u0, finishes = item_end <= end;
@@ -893,7 +943,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
         __syncwarp();
         if (lane == 0) {
           ws.cbase = item_end;
-          i4_next(p, ws.c);
+          i4_next(p, ws.c, UNIT);
         }
         __syncwarp();
       }
@@ -1050,7 +1100,7 @@ int run_int4(void* out, const void* q, const int32_t* query_start, const void* k
   const int group = num_q_heads / num_kv_heads;
   if (block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
   if (!rows_supported(group, head_dim)) return PA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(max_blocks) * block_size > INT32_MAX - I4_UNIT) return PA_ERR_SHAPE;
+  if (static_cast<long long>(max_blocks) * block_size > INT32_MAX - 256) return PA_ERR_SHAPE;
   if (num_seqs == 0 || total_rows == 0) return PA_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !workspace) return PA_ERR_NULL;
   const auto ok = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
