@@ -478,53 +478,75 @@ def pa_decode_static_scratch(out, q, k_cache, v_cache, block_tables, context_len
 
 
 # ---- the step around the attention -------------------------------------------------
-class _Args:
-    """Checks the tensors of one call and collects their device: all on one
-    CUDA device, which is made current for the launch if it is not."""
-    __slots__ = ("device",)
+# These calls run once or more per layer and step, and the small ones take less time on the GPU than a check of
+# twenty tensors can take here: the checks below are few attribute reads, and say what is wrong only when something is.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda d: torch.cuda.current_stream(d).cuda_stream)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_Tensor, _BF16, _F32, _I32, _U8 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
-    def __init__(self, first):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError("the tensors must be on a CUDA device")
-        self.device = first.get_device()
 
-    def ptr(self, t, name, dtype, shape, strided=False):
-        """Device pointer of t, which must have this dtype and shape (None: any
-        extent) and be contiguous -- or, strided, contiguous in all but its first dimension."""
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != self.device:
-            raise ValueError(f"{name} must be on the CUDA device of the call's other tensors")
-        got = t.shape
-        if len(got) != len(shape) or any(n is not None and n != g for n, g in zip(shape, got)):
-            raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, "
-                             f"got {tuple(got)}")
-        if not t.is_contiguous() and not (strided and (got[0] == 0 or t[0].is_contiguous())):
-            raise ValueError(f"{name} must be contiguous" + (" within each row" if strided else ""))
+def _device_of(t, name: str) -> int:
+    """Index of the CUDA device of a call's first tensor; all its tensors must be there."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return dev
+
+
+def _refuse(t, name, dtype, dev, shape, layout):
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the CUDA device of the call's other tensors")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be {layout}")
+
+
+def _at(t, name, dtype, dev, shape) -> int:
+    """Device pointer of a contiguous tensor of this type, device and shape."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+            and t.is_contiguous():
         return t.data_ptr()
-
-    def status(self, dev_status):
-        if dev_status is None:
-            return None
-        return self.ptr(dev_status, "dev_status", torch.int32, (1,))
-
-    def call(self, fn, stream, *args):
-        """fn(*args, stream) with the tensors' device current, on `stream` or that device's current one."""
-        if torch.cuda.current_device() == self.device:
-            s = torch.cuda.current_stream().cuda_stream if stream is None else _stream_ptr(stream)
-            rc = fn(*args, s)
-        else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, _stream_ptr(stream))
-        if rc != PA_OK:
-            _check(rc)
+    _refuse(t, name, dtype, dev, shape, "contiguous")
 
 
-def _row_stride(t, width):
-    """Elements from one row of t to the next (a single row's stride means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else width
+def _rows_at(t, name, dtype, dev, shape):
+    """Device pointer and row stride (elements) of a tensor whose rows are contiguous."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+        if t.is_contiguous():
+            return t.data_ptr(), width
+        st = t.stride()
+        if st[-1] == 1 and (len(st) == 2 or st[1] == shape[2] or shape[1] == 1):
+            return t.data_ptr(), st[0] if shape[0] > 1 else width
+    _refuse(t, name, dtype, dev, shape, "contiguous within each row")
+
+
+def _status_at(dev_status, dev):
+    return None if dev_status is None else _at(dev_status, "dev_status", _I32, dev, (1,))
+
+
+def _shape(t, name, ndim):
+    if not isinstance(t, _Tensor) or t.dim() != ndim:
+        raise ValueError(f"{name} must be a tensor of {ndim} dimensions")
+    return t.shape
+
+
+def _call(fn, dev, stream, *args) -> None:
+    """fn(*args, stream) with device `dev` current, on `stream` or that device's current one."""
+    if _current_device() == dev:
+        rc = fn(*args, _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if rc != PA_OK:
+        _check(rc)
 
 
 def pa_step_slots(new_tokens, context_lens, blocks_held, block_tables, free_blocks, free_state, block_size,
@@ -542,17 +564,19 @@ def pa_step_slots(new_tokens, context_lens, blocks_held, block_tables, free_bloc
         blocks_held_out = blocks_held
     if free_state_out is None:
         free_state_out = free_state
-    a, i32 = _Args(new_tokens), torch.int32
-    b = new_tokens.shape[0] if new_tokens.dim() else 0
-    t = positions.shape[0] if isinstance(positions, torch.Tensor) and positions.dim() else 0
-    a.call(_lib.pa_step_slots, stream, a.ptr(new_tokens, "new_tokens", i32, (b,)),
-           a.ptr(context_lens, "context_lens", i32, (b,)), a.ptr(context_lens_out, "context_lens_out", i32, (b,)),
-           a.ptr(blocks_held, "blocks_held", i32, (b,)), a.ptr(blocks_held_out, "blocks_held_out", i32, (b,)),
-           a.ptr(block_tables, "block_tables", i32, (b, None)), block_tables.shape[1],
-           a.ptr(free_blocks, "free_blocks", i32, (None,)), a.ptr(free_state, "free_state", i32, (2,)),
-           a.ptr(free_state_out, "free_state_out", i32, (2,)), b, free_blocks.shape[0], int(block_size),
-           a.ptr(query_start, "query_start", i32, (b + 1,)), a.ptr(positions, "positions", i32, (t,)),
-           a.ptr(slot_mapping, "slot_mapping", i32, (t,)), t, a.status(dev_status))
+    dev = _device_of(new_tokens, "new_tokens")
+    (b,), (t,), (nb,) = _shape(new_tokens, "new_tokens", 1), _shape(positions, "positions", 1), _shape(
+        free_blocks, "free_blocks", 1)
+    width = _shape(block_tables, "block_tables", 2)[1]
+    _call(_lib.pa_step_slots, dev, stream, _at(new_tokens, "new_tokens", _I32, dev, (b,)),
+          _at(context_lens, "context_lens", _I32, dev, (b,)),
+          _at(context_lens_out, "context_lens_out", _I32, dev, (b,)),
+          _at(blocks_held, "blocks_held", _I32, dev, (b,)), _at(blocks_held_out, "blocks_held_out", _I32, dev, (b,)),
+          _at(block_tables, "block_tables", _I32, dev, (b, width)), width,
+          _at(free_blocks, "free_blocks", _I32, dev, (nb,)), _at(free_state, "free_state", _I32, dev, (2,)),
+          _at(free_state_out, "free_state_out", _I32, dev, (2,)), b, nb, block_size,
+          _at(query_start, "query_start", _I32, dev, (b + 1,)), _at(positions, "positions", _I32, dev, (t,)),
+          _at(slot_mapping, "slot_mapping", _I32, dev, (t,)), t, _status_at(dev_status, dev))
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}  # pa_rope_type of include/pa.h
@@ -566,33 +590,31 @@ def pa_rope_table(table, base=10000.0, scaling="none", factor=1.0, original_posi
     include/pa.h."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
-    a = _Args(table)
-    p = a.ptr(table, "table", torch.float32, (None, None))
+    dev = _device_of(table, "table")
+    shape = _shape(table, "table", 2)
     sc = RopeScaling(ROPE_SCALINGS[scaling], int(original_positions), float(factor), 1.0 if low is None else float(low),
                      (4.0 if scaling == "bands" else 32.0) if high is None else float(high), float(attention_factor))
-    a.call(_lib.pa_rope_table, stream, p, table.shape[0], table.shape[1], float(base), ctypes.byref(sc))
+    _call(_lib.pa_rope_table, dev, stream, _at(table, "table", _F32, dev, shape), shape[0], shape[1], float(base),
+          ctypes.byref(sc))
 
 
-def _rope_call(fn, cache_dtype, cache_width, q_out, q, k_new, v_new, k_cache, v_cache, table, positions, slot_mapping,
+def _rope_call(fn, cache_dtype, int4, q_out, q, k_new, v_new, k_cache, v_cache, table, positions, slot_mapping,
                interleaved, scales, dev_status, stream):
-    a, bf, i32 = _Args(q), torch.bfloat16, torch.int32
-    if q.dim() != 3 or not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
-        raise ValueError("q must be [T, Hq, d] and k_new [T, Hkv, d]")
-    t, hq, d = q.shape
-    hkv = k_new.shape[1]
-    kc = a.ptr(k_cache, "k_cache", cache_dtype, (None, hkv, None, cache_width(d)))
-    a.call(fn, stream, a.ptr(q_out, "q_out", bf, (t, hq, d)), a.ptr(q, "q", bf, (t, hq, d), True),
-           _row_stride(q, hq * d), a.ptr(k_new, "k_new", bf, (t, hkv, d), True), _row_stride(k_new, hkv * d),
-           a.ptr(v_new, "v_new", bf, (t, hkv, d), True), _row_stride(v_new, hkv * d), kc,
-           a.ptr(v_cache, "v_cache", cache_dtype, tuple(k_cache.shape)),
-           a.ptr(table, "table", torch.float32, (None, None)), table.shape[0], table.shape[1], 1 if interleaved else 0,
-           a.ptr(positions, "positions", i32, (t,)), a.ptr(slot_mapping, "slot_mapping", i32, (t,)), t,
-           k_cache.shape[0], hq, hkv, d, k_cache.shape[2], *scales, a.status(dev_status))
-
-
-def _int4_width(d):
-    """Bytes of a head's row of d values in a 4-bit cache: codes and scales."""
-    return d * 9 // 16
+    dev = _device_of(q, "q")
+    t, hq, d = shape = _shape(q, "q", 3)
+    hkv = _shape(k_new, "k_new", 3)[1]
+    new = (t, hkv, d)
+    nb, _, bs, _ = _shape(k_cache, "k_cache", 4)
+    cache = (nb, hkv, bs, d * 9 // 16 if int4 else d)
+    length, rot = _shape(table, "table", 2)
+    qp, qs = _rows_at(q, "q", _BF16, dev, shape)
+    kp, ks = _rows_at(k_new, "k_new", _BF16, dev, new)
+    vp, vs = _rows_at(v_new, "v_new", _BF16, dev, new)
+    _call(fn, dev, stream, _at(q_out, "q_out", _BF16, dev, shape), qp, qs, kp, ks, vp, vs,
+          _at(k_cache, "k_cache", cache_dtype, dev, cache), _at(v_cache, "v_cache", cache_dtype, dev, cache),
+          _at(table, "table", _F32, dev, (length, rot)), length, rot, 1 if interleaved else 0,
+          _at(positions, "positions", _I32, dev, (t,)), _at(slot_mapping, "slot_mapping", _I32, dev, (t,)), t, nb, hq,
+          hkv, d, bs, *scales, _status_at(dev_status, dev))
 
 
 def pa_rope_append(q_out, q, k_new, v_new, k_cache, v_cache, table, positions, slot_mapping, interleaved=False,
@@ -601,50 +623,46 @@ def pa_rope_append(q_out, q, k_new, v_new, k_cache, v_cache, table, positions, s
     by table row positions[t]; v_new goes to the cache unrotated.  q, k_new and
     v_new may be views of one projection's output (contiguous within a token);
     q_out may be q.  See include/pa.h."""
-    _rope_call(_lib.pa_rope_append, torch.bfloat16, lambda d: d, q_out, q, k_new, v_new, k_cache, v_cache, table,
-               positions, slot_mapping, interleaved, (), dev_status, stream)
+    _rope_call(_lib.pa_rope_append, _BF16, False, q_out, q, k_new, v_new, k_cache, v_cache, table, positions,
+               slot_mapping, interleaved, (), dev_status, stream)
 
 
 def pa_rope_append_fp8(q_out, q, k_new, v_new, k_cache, v_cache, table, positions, slot_mapping, k_scale, v_scale,
                        interleaved=False, dev_status=None, stream=None) -> None:
     """pa_rope_append into an FP8 (E4M3 codes, uint8) cache with per-tensor scales."""
-    _rope_call(_lib.pa_rope_append_fp8, torch.uint8, lambda d: d, q_out, q, k_new, v_new, k_cache, v_cache, table,
-               positions, slot_mapping, interleaved, (float(k_scale), float(v_scale)), dev_status, stream)
+    _rope_call(_lib.pa_rope_append_fp8, _U8, False, q_out, q, k_new, v_new, k_cache, v_cache, table, positions,
+               slot_mapping, interleaved, (float(k_scale), float(v_scale)), dev_status, stream)
 
 
 def pa_rope_append_int4(q_out, q, k_new, v_new, k_cache, v_cache, table, positions, slot_mapping, interleaved=False,
                         dev_status=None, stream=None) -> None:
     """pa_rope_append into a 4-bit cache (uint8 [num_blocks, Hkv, block_size, d * 9 / 16])."""
-    _rope_call(_lib.pa_rope_append_int4, torch.uint8, _int4_width, q_out, q, k_new, v_new, k_cache, v_cache, table,
-               positions, slot_mapping, interleaved, (), dev_status, stream)
+    _rope_call(_lib.pa_rope_append_int4, _U8, True, q_out, q, k_new, v_new, k_cache, v_cache, table, positions,
+               slot_mapping, interleaved, (), dev_status, stream)
+
+
+def _int4_rows(fn, names, dtype, k, v, k_cache, v_cache, slot_mapping, dev_status, stream):
+    dev = _device_of(k, names[0])
+    t, hkv, d = shape = _shape(k, names[0], 3)
+    nb, _, bs, _ = _shape(k_cache, "k_cache", 4)
+    cache = (nb, hkv, bs, d * 9 // 16)
+    _call(fn, dev, stream, _at(k, names[0], dtype, dev, shape), _at(v, names[1], dtype, dev, shape),
+          _at(k_cache, "k_cache", _U8, dev, cache), _at(v_cache, "v_cache", _U8, dev, cache),
+          _at(slot_mapping, "slot_mapping", _I32, dev, (t,)), t, nb, hkv, d, bs, _status_at(dev_status, dev))
 
 
 def pa_cache_append_int4(k_new, v_new, k_cache, v_cache, slot_mapping, dev_status=None, stream=None) -> None:
     """Quantise k_new / v_new [T, Hkv, d] (bf16) into a 4-bit cache (uint8
     [num_blocks, Hkv, block_size, d * 9 / 16]) at slot_mapping [T]; see include/pa.h."""
-    a, bf = _Args(k_new), torch.bfloat16
-    if k_new.dim() != 3:
-        raise ValueError("k_new must be [T, Hkv, d]")
-    t, hkv, d = k_new.shape
-    kc = a.ptr(k_cache, "k_cache", torch.uint8, (None, hkv, None, _int4_width(d)))
-    a.call(_lib.pa_cache_append_int4, stream, a.ptr(k_new, "k_new", bf, (t, hkv, d)),
-           a.ptr(v_new, "v_new", bf, (t, hkv, d)), kc, a.ptr(v_cache, "v_cache", torch.uint8, tuple(k_cache.shape)),
-           a.ptr(slot_mapping, "slot_mapping", torch.int32, (t,)), t, k_cache.shape[0], hkv, d, k_cache.shape[2],
-           a.status(dev_status))
+    _int4_rows(_lib.pa_cache_append_int4, ("k_new", "v_new"), _BF16, k_new, v_new, k_cache, v_cache, slot_mapping,
+               dev_status, stream)
 
 
 def pa_cache_read_int4(k_out, v_out, k_cache, v_cache, slot_mapping, dev_status=None, stream=None) -> None:
     """The rows of a 4-bit cache in slot_mapping [T] as values: k_out / v_out
     [T, Hkv, d] (float32); rows of negative slots are left as they are."""
-    a, f = _Args(k_out), torch.float32
-    if k_out.dim() != 3:
-        raise ValueError("k_out must be [T, Hkv, d]")
-    t, hkv, d = k_out.shape
-    kc = a.ptr(k_cache, "k_cache", torch.uint8, (None, hkv, None, _int4_width(d)))
-    a.call(_lib.pa_cache_read_int4, stream, a.ptr(k_out, "k_out", f, (t, hkv, d)),
-           a.ptr(v_out, "v_out", f, (t, hkv, d)), kc, a.ptr(v_cache, "v_cache", torch.uint8, tuple(k_cache.shape)),
-           a.ptr(slot_mapping, "slot_mapping", torch.int32, (t,)), t, k_cache.shape[0], hkv, d, k_cache.shape[2],
-           a.status(dev_status))
+    _int4_rows(_lib.pa_cache_read_int4, ("k_out", "v_out"), _F32, k_out, v_out, k_cache, v_cache, slot_mapping,
+               dev_status, stream)
 
 
 def pa_int4_workspace_bytes(num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
@@ -663,24 +681,24 @@ def make_int4_workspace(num_q_heads: int, num_kv_heads: int, head_dim: int, devi
 
 def _int4_attention(fn, out, q, query_start, k_cache, v_cache, block_tables, context_lens, scale, workspace,
                     dev_status, stream):
-    a, i32 = _Args(q), torch.int32
-    if q.dim() != 3:
-        raise ValueError("q must be [rows, Hq, d]")
-    t, hq, d = q.shape
-    b = context_lens.shape[0] if isinstance(context_lens, torch.Tensor) and context_lens.dim() else 0
-    head = (a.ptr(out, "out", torch.bfloat16, (t, hq, d)), a.ptr(q, "q", torch.bfloat16, (t, hq, d)))
-    rows = ()
+    dev = _device_of(q, "q")
+    t, hq, d = shape = _shape(q, "q", 3)
+    (b,) = _shape(context_lens, "context_lens", 1)
+    width = _shape(block_tables, "block_tables", 2)[1]
+    nb, hkv, bs, _ = _shape(k_cache, "k_cache", 4)
+    cache = (nb, hkv, bs, d * 9 // 16)
+    op, qp = _at(out, "out", _BF16, dev, shape), _at(q, "q", _BF16, dev, shape)
     if query_start is not None:
-        head += (a.ptr(query_start, "query_start", i32, (b + 1,)),)
-        rows = (t,)
-    elif t != b:
+        head, rows = (op, qp, _at(query_start, "query_start", _I32, dev, (b + 1,))), (t,)
+    elif t == b:
+        head, rows = (op, qp), ()
+    else:
         raise ValueError("pa_decode_int4 takes exactly one query row per sequence")
-    kc = a.ptr(k_cache, "k_cache", torch.uint8, (None, None, None, _int4_width(d)))
-    nb, hkv, bs, _ = k_cache.shape
-    a.call(fn, stream, *head, kc, a.ptr(v_cache, "v_cache", torch.uint8, (nb, hkv, bs, _int4_width(d))),
-           a.ptr(block_tables, "block_tables", i32, (b, None)), block_tables.shape[1],
-           a.ptr(context_lens, "context_lens", i32, (b,)), b, *rows, hq, hkv, d, bs, nb, float(scale),
-           a.ptr(workspace, "workspace", torch.uint8, (None,)), workspace.shape[0], a.status(dev_status))
+    (size,) = _shape(workspace, "workspace", 1)
+    _call(fn, dev, stream, *head, _at(k_cache, "k_cache", _U8, dev, cache), _at(v_cache, "v_cache", _U8, dev, cache),
+          _at(block_tables, "block_tables", _I32, dev, (b, width)), width,
+          _at(context_lens, "context_lens", _I32, dev, (b,)), b, *rows, hq, hkv, d, bs, nb, float(scale),
+          _at(workspace, "workspace", _U8, dev, (size,)), size, _status_at(dev_status, dev))
 
 
 def pa_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, scale, workspace, dev_status=None,
@@ -707,29 +725,24 @@ def pa_accept_drafts(out_tokens, num_accepted, target_probs, draft_probs, tokens
     row, query_start [B + 1], uniforms [rows] in [0, 1).  out_tokens [rows] and
     num_accepted [B] are written; context_lens [B], if given, lose the rows not
     kept (in place, or into context_lens_out).  See include/pa.h."""
-    a, i32 = _Args(target_probs), torch.int32
-    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+    dev = _device_of(target_probs, "target_probs")
+    dtype = target_probs.dtype
+    if dtype is not _F32 and dtype is not _BF16:
         raise TypeError("target_probs must be float32 or bfloat16")
-    if target_probs.dim() != 2:
-        raise ValueError("target_probs must be [rows, vocab]")
-    r, v = target_probs.shape
-    b = num_accepted.shape[0] if isinstance(num_accepted, torch.Tensor) and num_accepted.dim() else 0
-    if context_lens is None and context_lens_out is not None:
+    r, v = shape = _shape(target_probs, "target_probs", 2)
+    (b,) = _shape(num_accepted, "num_accepted", 1)
+    cp = co = None
+    if context_lens is not None:
+        cp = _at(context_lens, "context_lens", _I32, dev, (b,))
+        co = cp if context_lens_out is None else _at(context_lens_out, "context_lens_out", _I32, dev, (b,))
+    elif context_lens_out is not None:
         raise ValueError("context_lens_out needs context_lens")
-    if context_lens_out is None:
-        context_lens_out = context_lens
-    dp, ds = None, 0
-    if draft_probs is not None:
-        dp = a.ptr(draft_probs, "draft_probs", target_probs.dtype, (r, v), True)
-        ds = _row_stride(draft_probs, v)
-    a.call(_lib.pa_accept_drafts, stream, a.ptr(out_tokens, "out_tokens", i32, (r,)),
-           a.ptr(num_accepted, "num_accepted", i32, (b,)),
-           a.ptr(target_probs, "target_probs", target_probs.dtype, (r, v), True), _row_stride(target_probs, v), dp, ds,
-           int(target_probs.dtype is torch.bfloat16), a.ptr(tokens, "tokens", i32, (r,)),
-           a.ptr(query_start, "query_start", i32, (b + 1,)), a.ptr(uniforms, "uniforms", torch.float32, (r,)), b, r, v,
-           None if context_lens is None else a.ptr(context_lens, "context_lens", i32, (b,)),
-           None if context_lens is None else a.ptr(context_lens_out, "context_lens_out", i32, (b,)),
-           a.status(dev_status))
+    tp, ts = _rows_at(target_probs, "target_probs", dtype, dev, shape)
+    dp, ds = (None, 0) if draft_probs is None else _rows_at(draft_probs, "draft_probs", dtype, dev, shape)
+    _call(_lib.pa_accept_drafts, dev, stream, _at(out_tokens, "out_tokens", _I32, dev, (r,)),
+          _at(num_accepted, "num_accepted", _I32, dev, (b,)), tp, ts, dp, ds, 1 if dtype is _BF16 else 0,
+          _at(tokens, "tokens", _I32, dev, (r,)), _at(query_start, "query_start", _I32, dev, (b + 1,)),
+          _at(uniforms, "uniforms", _F32, dev, (r,)), b, r, v, cp, co, _status_at(dev_status, dev))
 
 
 def exported_symbols() -> list[str]:

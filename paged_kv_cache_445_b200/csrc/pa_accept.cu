@@ -11,7 +11,7 @@
 //
 // Only the rows that decide a draw are read whole: one target row and, after a
 // refusal, one draft row per sequence, V values each, so HBM bounds a full
-// batch and latency a single chat.  One cluster of 8 CTAs per sequence: 128
+// batch and latency a single chat.  One cluster of 2 to 8 CTAs per sequence: its
 // warps take contiguous slices of the vocabulary, their sums meet in
 // distributed shared memory, and the warp whose slice holds the draw scans it
 // again (from L1/L2).  No workspace, no atomics; sums are binary64, so the
@@ -28,10 +28,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int ACC_CTAS = 8;      // per sequence (one cluster)
 constexpr int ACC_THREADS = 512;
 constexpr int ACC_WARPS = ACC_THREADS / 32;
-constexpr int ACC_SLICES = ACC_CTAS * ACC_WARPS;
 
 struct AcceptParams {
   int32_t* out_tokens;
@@ -51,23 +49,64 @@ struct AcceptParams {
 __device__ __forceinline__ float prob(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float prob(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
+__device__ __forceinline__ float value_of(float x) { return x; }
+__device__ __forceinline__ float value_of(__nv_bfloat16 x) { return __bfloat162float(x); }
+
 // Which weights a draw uses.
 enum Mode { FROM_TARGET, FROM_DIFFERENCE, FROM_OTHERS };
 
-// Weight of token v: the target's probability, what the draft leaves of it, or
-// zero for the refused token.  Negative, infinite and NaN values weigh nothing.
+// A weight from the target's value and what is taken off it; negative, infinite and NaN ones weigh nothing.  Signs
+// and ranges are told in binary32, where they are exact, the difference is taken in binary64, where it is.
+__device__ __forceinline__ double weight_of(float t, float d) {
+  const bool ok = t > d && t < INFINITY && d > -INFINITY;
+  return static_cast<double>(ok ? t : 0.f) - static_cast<double>(ok ? d : 0.f);
+}
 template <class T>
 __device__ __forceinline__ double weight(Mode mode, const T* t, const T* d, int refused, int v) {
-  double w = prob(t + v);
-  if (mode == FROM_DIFFERENCE) w -= static_cast<double>(prob(d + v));
-  if (mode == FROM_OTHERS && v == refused) w = 0.0;
-  return w > 0.0 && w < INFINITY ? w : 0.0;
+  if (mode == FROM_OTHERS && v == refused) return 0.0;
+  return weight_of(prob(t + v), mode == FROM_DIFFERENCE ? prob(d + v) : 0.f);
 }
 
-template <class T>
-__global__ void __launch_bounds__(ACC_THREADS) accept_kernel(const AcceptParams p) {
+// Sum of the weights of [lo, hi) over the warp's lanes: max(t, d) - d, five instructions a value (binary64
+// conversions bound the loop otherwise).  What may not weigh (NaN, infinities) shows in the sum, and the slice is then
+// taken again with weight().  VEC values (16 bytes) per load.
+template <class T, int VEC, bool DIFF>
+__device__ __forceinline__ double slice_sum(const T* t, const T* d, int lo, int hi, int lane) {
+  constexpr int STEP = 32 * VEC, UNROLL = 4;
+  double sum = 0.0;
+  const auto add = [&](T x, T y) {
+    const float a = value_of(x), b = DIFF ? value_of(y) : 0.f;
+    sum += DIFF ? static_cast<double>(fmaxf(a, b)) - static_cast<double>(b) : static_cast<double>(fmaxf(a, 0.f));
+  };
+  int v0 = lo + lane * VEC;
+  for (; v0 - lane * VEC + STEP * UNROLL <= hi; v0 += STEP * UNROLL) {
+    uint4 a[UNROLL], b[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      if constexpr (VEC > 1) {
+        a[u] = __ldg(reinterpret_cast<const uint4*>(t + v0 + u * STEP));
+        if (DIFF) b[u] = __ldg(reinterpret_cast<const uint4*>(d + v0 + u * STEP));
+      } else {
+        *reinterpret_cast<T*>(&a[u]) = t[v0 + u * STEP];
+        if (DIFF) *reinterpret_cast<T*>(&b[u]) = d[v0 + u * STEP];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) add(reinterpret_cast<const T*>(&a[u])[k], reinterpret_cast<const T*>(&b[u])[k]);
+  }
+  for (int v = v0 - lane * VEC + lane; v < hi; v += 32) add(t[v], DIFF ? d[v] : T(0.f));
+  return sum;
+}
+
+// CTAS: CTAs per sequence, one cluster.
+template <class T, int CTAS>
+__global__ void __launch_bounds__(ACC_THREADS, 2) accept_kernel(const AcceptParams p) {
+  constexpr int ACC_CTAS = CTAS, ACC_SLICES = CTAS * ACC_WARPS;
   __shared__ double sums[2][ACC_SLICES];  // double-buffered over the two passes a draw may take
-  __shared__ int lasts[2][ACC_SLICES];    // last index with a weight in each slice, -1: none
+  __shared__ int lasts[ACC_SLICES];       // last index with a weight in each slice, -1: none
+  __shared__ double parts[ACC_WARPS];
   __shared__ int sh_acc, sh_mode, sh_refused;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
@@ -141,44 +180,40 @@ __global__ void __launch_bounds__(ACC_THREADS) accept_kernel(const AcceptParams 
   const int hi = static_cast<int>(lo64 + per < p.vocab ? lo64 + per : p.vocab);
   cluster.barrier_wait();
   double total = 0.0, before = 0.0, u = 0.0;
-  int owner = -1, last = -1;
+  int owner = -1;
   for (int pass = 0; pass < 2; ++pass) {
     double sum = 0.0;
-    int at = -1;
-    for (int v = lo + lane; v < hi; v += 32) {
-      const double w = weight(mode, t, d, refused, v);
-      sum += w;
-      if (w > 0.0) at = v;
+    // (slices start at multiples of 128)
+    const uintptr_t at = reinterpret_cast<uintptr_t>(t) | (mode == FROM_DIFFERENCE ? reinterpret_cast<uintptr_t>(d) : 0);
+    constexpr int VEC = 16 / sizeof(T);
+    if (mode == FROM_DIFFERENCE)
+      sum = at % 16 == 0 ? slice_sum<T, VEC, true>(t, d, lo, hi, lane) : slice_sum<T, 1, true>(t, d, lo, hi, lane);
+    else
+      sum = at % 16 == 0 ? slice_sum<T, VEC, false>(t, d, lo, hi, lane) : slice_sum<T, 1, false>(t, d, lo, hi, lane);
+    const bool odd = !(sum < INFINITY) || (mode == FROM_OTHERS && refused >= lo && refused < hi);
+    if (__any_sync(FULL_MASK, odd)) {
+      sum = 0.0;
+      for (int v = lo + lane; v < hi; v += 32) sum += weight(mode, t, d, refused, v);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      sum += __shfl_xor_sync(FULL_MASK, sum, o);
-      at = max(at, __shfl_xor_sync(FULL_MASK, at, o));
-    }
-    if (lane < ACC_CTAS) {  // to every CTA of the cluster
-      cluster.map_shared_rank(&sums[pass][mine], lane)[0] = sum;
-      cluster.map_shared_rank(&lasts[pass][mine], lane)[0] = at;
-    }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
+    if (lane < ACC_CTAS) *cluster.map_shared_rank(&sums[pass][mine], lane) = sum;  // to every CTA of the cluster
     cluster.sync();
     // every warp finds the slice that holds the draw
     double c[ACC_SLICES / 32], run = 0.0;
-    int l = -1;
 #pragma unroll
     for (int k = 0; k < ACC_SLICES / 32; ++k) {
       const int j = lane * (ACC_SLICES / 32) + k;
       run += sums[pass][j];
       c[k] = run;
-      l = max(l, lasts[pass][j]);
     }
     double pre = run;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double x = __shfl_up_sync(FULL_MASK, pre, o);
       if (lane >= o) pre += x;
-      l = max(l, __shfl_xor_sync(FULL_MASK, l, o));
     }
     total = __shfl_sync(FULL_MASK, pre, 31);
-    last = l;
     u = static_cast<double>(p.uniforms[end - 1]) * total;
     pre = __shfl_up_sync(FULL_MASK, pre, 1);  // sum before this lane's slices
     if (lane == 0) pre = 0.0;
@@ -186,7 +221,7 @@ __global__ void __launch_bounds__(ACC_THREADS) accept_kernel(const AcceptParams 
     double hit_before = 0.0;
 #pragma unroll
     for (int k = ACC_SLICES / 32 - 1; k >= 0; --k)
-      if (pre + c[k] > u && lasts[pass][lane * (ACC_SLICES / 32) + k] >= 0) {
+      if (pre + c[k] > u && sums[pass][lane * (ACC_SLICES / 32) + k] > 0.0) {
         hit = lane * (ACC_SLICES / 32) + k;
         hit_before = pre + (k > 0 ? c[k - 1] : 0.0);
       }
@@ -208,48 +243,79 @@ __global__ void __launch_bounds__(ACC_THREADS) accept_kernel(const AcceptParams 
     }
   }
   if (owner < 0) {  // u times the total is not passed (rounding, u >= 1): the last token with a weight
-    if (rank == 0 && tid == 0) {
-      p.out_tokens[start + acc] = last;
-      if (last < 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
+    int last = -1;
+    for (int v = lo + lane; v < hi; v += 32)
+      if (weight(mode, t, d, refused, v) > 0.0) last = v;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) last = max(last, __shfl_xor_sync(FULL_MASK, last, o));
+    if (lane == 0) *cluster.map_shared_rank(&lasts[mine], 0) = last;
+    cluster.sync();
+    if (rank == 0 && warp == 0) {
+      last = -1;
+      for (int j = lane; j < ACC_SLICES; j += 32) last = max(last, lasts[j]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) last = max(last, __shfl_xor_sync(FULL_MASK, last, o));
+      if (lane == 0) {
+        p.out_tokens[start + acc] = last;
+        if (last < 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
+      }
     }
-  } else if (owner == mine) {
-    int token = -1;
-    double sum = before;
-    for (int v0 = lo; v0 < hi && token < 0; v0 += 128) {
-      double w[4], run = 0.0;
+  } else if (owner / ACC_WARPS == rank) {
+    // The slice that holds the draw, again: its CTA's warps take a part each, the one whose part passes u scans it.
+    const long long from = static_cast<long long>(owner) * per;
+    const int to = static_cast<int>(from + per < p.vocab ? from + per : p.vocab);
+    const int part = (to - static_cast<int>(from) + ACC_WARPS * 128 - 1) / (ACC_WARPS * 128) * 128;
+    const int a = min(static_cast<int>(from) + warp * part, to), b = min(a + part, to);
+    double sum = 0.0;
+    for (int v = a + lane; v < b; v += 32) sum += weight(mode, t, d, refused, v);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int v = v0 + lane * 4 + k;
-        w[k] = v < hi ? weight(mode, t, d, refused, v) : 0.0;
-        run += w[k];
-      }
-      double pre = run;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(FULL_MASK, pre, o);
-        if (lane >= o) pre += x;
-      }
-      const double all = __shfl_sync(FULL_MASK, pre, 31);
-      double at = __shfl_up_sync(FULL_MASK, pre, 1);
-      at = sum + (lane == 0 ? 0.0 : at);
-      int hit = -1;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        at += w[k];
-        if (hit < 0 && w[k] > 0.0 && at > u) hit = v0 + lane * 4 + k;
-      }
-      const unsigned m = __ballot_sync(FULL_MASK, hit >= 0);
-      if (m) token = __shfl_sync(FULL_MASK, hit, __ffs(m) - 1);
-      sum += all;
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
+    if (lane == 0) parts[warp] = sum;
+    __syncthreads();
+    int win = -1;  // rounding may leave no part past u: then the last one with a weight
+    double run = before, at = before;
+    for (int w = 0; w < ACC_WARPS; ++w) {
+      if (parts[w] > 0.0 && (win < 0 || !(at + parts[win] > u))) win = w, at = run;
+      run += parts[w];
     }
-    if (lane == 0) {
-      const int slice_last = lasts[mode == static_cast<Mode>(sh_mode) ? 0 : 1][mine];
-      p.out_tokens[start + acc] = token >= 0 ? token : slice_last;
+    if (win == warp) {
+      int token = -1, last = -1;
+      for (int v0 = a; v0 < b && token < 0; v0 += 128) {
+        double w[4], mine4 = 0.0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int v = v0 + lane * 4 + k;
+          w[k] = v < b ? weight(mode, t, d, refused, v) : 0.0;
+          mine4 += w[k];
+        }
+        double pre = mine4;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double x = __shfl_up_sync(FULL_MASK, pre, o);
+          if (lane >= o) pre += x;
+        }
+        const double all = __shfl_sync(FULL_MASK, pre, 31);
+        double c = __shfl_up_sync(FULL_MASK, pre, 1);
+        c = at + (lane == 0 ? 0.0 : c);
+        int hit = -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          c += w[k];
+          if (w[k] > 0.0) last = v0 + lane * 4 + k;
+          if (hit < 0 && w[k] > 0.0 && c > u) hit = v0 + lane * 4 + k;
+        }
+        const unsigned m = __ballot_sync(FULL_MASK, hit >= 0);
+        if (m) token = __shfl_sync(FULL_MASK, hit, __ffs(m) - 1);
+        at += all;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) last = max(last, __shfl_xor_sync(FULL_MASK, last, o));
+      if (lane == 0) p.out_tokens[start + acc] = token >= 0 ? token : last;
     }
   }
 }
 
-template <class T>
+template <class T, int ACC_CTAS>
 int launch_accept(const AcceptParams& p, int num_seqs, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * ACC_CTAS);
@@ -262,7 +328,7 @@ int launch_accept(const AcceptParams& p, int num_seqs, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return check_launch(cudaLaunchKernelEx(&cfg, accept_kernel<T>, p), "accept_kernel launch");
+  return check_launch(cudaLaunchKernelEx(&cfg, accept_kernel<T, ACC_CTAS>, p), "accept_kernel launch");
 }
 
 }  // namespace
@@ -277,7 +343,7 @@ extern "C" int pa_accept_drafts(int32_t* out_tokens, int32_t* num_accepted, cons
                                 void* stream) {
   if (num_seqs < 0 || total_rows < 0 || vocab <= 0 || target_stride < vocab) return PA_ERR_SHAPE;
   if (draft_probs && draft_stride < vocab) return PA_ERR_SHAPE;
-  if (num_seqs > INT32_MAX / pa::ACC_CTAS) return PA_ERR_SHAPE;
+  if (num_seqs > INT32_MAX / 8) return PA_ERR_SHAPE;
   if ((context_lens == nullptr) != (context_lens_out == nullptr)) return PA_ERR_NULL;
   if (num_seqs == 0) return PA_OK;
   if (!num_accepted || !query_start) return PA_ERR_NULL;
@@ -288,5 +354,11 @@ extern "C" int pa_accept_drafts(int32_t* out_tokens, int32_t* num_accepted, cons
   pa::AcceptParams p{out_tokens, num_accepted, target_probs, draft_probs, target_stride, draft_stride, tokens,
                      query_start, uniforms, context_lens, context_lens_out, total_rows, vocab, dev_status};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return probs_bf16 ? pa::launch_accept<__nv_bfloat16>(p, num_seqs, st) : pa::launch_accept<float>(p, num_seqs, st);
+  // As many CTAs a sequence as keep the batch in one wave (two CTAs fit an SM), 8 at most.  128 sequences of 128,000
+  // values: 2 take 26 us, 4 take 29.
+  const int room = 2 * di.num_sms / num_seqs;
+  const auto launch = room >= 8   ? probs_bf16 ? pa::launch_accept<__nv_bfloat16, 8> : pa::launch_accept<float, 8>
+                      : room >= 4 ? probs_bf16 ? pa::launch_accept<__nv_bfloat16, 4> : pa::launch_accept<float, 4>
+                                  : probs_bf16 ? pa::launch_accept<__nv_bfloat16, 2> : pa::launch_accept<float, 2>;
+  return launch(p, num_seqs, st);
 }

@@ -11,12 +11,12 @@
 // Row t of sequence s then has position ctx + i and slot table[pos / bs] * bs
 // + pos % bs, where a new block's ID is read straight from the queue.
 //
-// A few bytes per row: bound by launch and dependent-load latency.  One
-// thread-block cluster of up to 8 CTAs: every CTA scans the whole batch (tiles
-// of 1024 sequences, one per thread) and writes its share of the rows, found
-// by binary search in the tile's row ends.  The lengths and the queue state
-// may be updated in place, so they are written only after the cluster barrier
-// that ends every CTA's reads.
+// A few bytes per row: bound by launch and dependent-load latency.  Every CTA
+// scans the whole batch (tiles of one sequence per thread) and writes its share
+// of the rows, found by binary search in the tile's row ends.  The lengths and
+// the queue state may be updated in place, so they are written only when every
+// CTA has read them: after the barrier of one cluster of up to 8 CTAs, or, for
+// row buffers that keep more CTAs busy, by a second launch.
 #include <cooperative_groups.h>
 
 #include "pa_device.cuh"
@@ -28,8 +28,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int SLOT_THREADS = 1024;
-constexpr int SLOT_MAX_CTAS = 8;
+constexpr int SLOT_MAX_CTAS = 8;        // of a cluster
+constexpr int SLOT_ROWS_PER_CTA = 2048;  // below that a second CTA only repeats the scan
+
+enum SlotsPart { SLOTS_ROWS = 1, SLOTS_STATE = 2 };  // what a launch writes
 
 struct SlotsParams {
   const int32_t* new_tokens;
@@ -60,13 +62,14 @@ struct Carry {
   long long rows, need, back;
 };
 
+template <int THREADS>
 struct SlotsShared {
-  long long warp[3][32];
-  long long rows_end[SLOT_THREADS];  // inclusive prefix of the rows
-  int ctx[SLOT_THREADS];
-  int held[SLOT_THREADS];            // -1: the sequence is refused
-  int first[SLOT_THREADS];           // queue place of its first new block
-  int taken;                         // blocks taken so far
+  long long warp[3][THREADS / 32];
+  long long rows_end[THREADS];  // inclusive prefix of the rows
+  int ctx[THREADS];
+  int held[THREADS];            // -1: the sequence is refused
+  int first[THREADS];           // queue place of its first new block
+  int taken;                    // blocks taken so far
 };
 
 __device__ __forceinline__ long long warp_inclusive(long long v, int lane) {
@@ -79,7 +82,8 @@ __device__ __forceinline__ long long warp_inclusive(long long v, int lane) {
 }
 
 // Load sequence s of the tile and scan the tile; `carry` moves to its end.
-__device__ Seq scan_tile(const SlotsParams& p, SlotsShared& sh, int s, int count, bool bad_queue, Carry& carry) {
+template <int THREADS>
+__device__ Seq scan_tile(const SlotsParams& p, SlotsShared<THREADS>& sh, int s, int count, bool bad_queue, Carry& carry) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Seq q{};
   int bits = 0;
@@ -110,7 +114,7 @@ __device__ Seq scan_tile(const SlotsParams& p, SlotsShared& sh, int s, int count
   __syncthreads();
   long long base = carry.rows, total = 0;
 #pragma unroll 8
-  for (int w = 0; w < SLOT_THREADS / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     const long long x = sh.warp[0][w];
     base += w < warp ? x : 0;
     total += x;
@@ -131,7 +135,7 @@ __device__ Seq scan_tile(const SlotsParams& p, SlotsShared& sh, int s, int count
   __syncthreads();
   long long nb = carry.need, nt = 0, bb = carry.back, bt = 0;
 #pragma unroll 8
-  for (int w = 0; w < SLOT_THREADS / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     const long long x = sh.warp[1][w], y = sh.warp[2][w];
     nb += w < warp ? x : 0;
     nt += x;
@@ -155,14 +159,16 @@ __device__ __forceinline__ void write_seq(const SlotsParams& p, int s, const Seq
   p.blocks_held_out[s] = q.held + (q.served ? q.need : 0) - q.back;
 }
 
-__global__ void __launch_bounds__(SLOT_THREADS) slots_kernel(const SlotsParams p) {
-  __shared__ SlotsShared sh;
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) slots_kernel(const SlotsParams p, int parts) {
+  constexpr int SLOT_THREADS = THREADS;
+  __shared__ SlotsShared<THREADS> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x, ctas = gridDim.x;
   int head = p.free_state[0], count = p.free_state[1];
   const bool bad_queue = head < 0 || head >= p.num_blocks || count < 0 || count > p.num_blocks;
   if (bad_queue) {
-    if (tid == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
+    if (tid == 0 && (parts & SLOTS_ROWS)) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
     head = count = 0;
   }
   if (tid == 0) sh.taken = 0;
@@ -172,7 +178,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) slots_kernel(const SlotsParams p
   const int bs = 1 << p.block_shift;
   Seq q{};
   if (rank == 0 && tid == 0) p.query_start[0] = 0;
-  for (int tile = 0; tile < tiles; ++tile) {
+  for (int tile = 0; tile < tiles && (parts & SLOTS_ROWS); ++tile) {
     const int s = tile * SLOT_THREADS + tid;
     const long long first_row = carry.rows;
     q = scan_tile(p, sh, s, count, bad_queue, carry);
@@ -240,17 +246,20 @@ __global__ void __launch_bounds__(SLOT_THREADS) slots_kernel(const SlotsParams p
     __syncthreads();
   }
   // rows behind the last sequence are padding
-  for (long long t = carry.rows + rank * SLOT_THREADS + tid; t < p.max_tokens; t += ctas * SLOT_THREADS) {
-    p.positions[t] = -1;
-    p.slots[t] = -1;
+  if (parts & SLOTS_ROWS) {
+    for (long long t = carry.rows + rank * SLOT_THREADS + tid; t < p.max_tokens; t += ctas * SLOT_THREADS) {
+      p.positions[t] = -1;
+      p.slots[t] = -1;
+    }
   }
+  if (!(parts & SLOTS_STATE)) return;
   // every CTA has read the lengths and the queue state: now they may change
-  __threadfence();
-  cg::this_cluster().sync();
-  if (rank != 0) return;
-  const int taken = sh.taken;
-  const long long back = carry.back;
-  if (tiles == 1) {
+  if (parts & SLOTS_ROWS) {
+    __threadfence();
+    cg::this_cluster().sync();
+    if (rank != 0) return;
+  }
+  if (tiles == 1 && (parts & SLOTS_ROWS)) {
     write_seq(p, tid, q);
   } else {
     carry = Carry{0, 0, 0};
@@ -263,8 +272,10 @@ __global__ void __launch_bounds__(SLOT_THREADS) slots_kernel(const SlotsParams p
       __syncthreads();
     }
   }
+  __syncthreads();
   if (tid == 0) {
-    const long long left = count - taken + back;
+    const int taken = sh.taken;
+    const long long left = count - taken + carry.back;
     int at = head + taken;
     if (at >= p.num_blocks) at -= p.num_blocks;
     if (!bad_queue) {
@@ -304,13 +315,20 @@ extern "C" int pa_step_slots(const int32_t* new_tokens, const int32_t* context_l
   pa::SlotsParams p{new_tokens,     context_lens, blocks_held, context_lens_out, blocks_held_out, block_tables,
                     free_blocks,    free_state,   free_state_out, query_start,   positions,       slot_mapping,
                     num_seqs,       max_blocks_per_seq, num_blocks, block_size == 16 ? 4 : 5, max_tokens, dev_status};
-  // one CTA per 2048 rows: below that a second CTA only repeats the scan
-  int ctas = 1;
-  while (ctas < pa::SLOT_MAX_CTAS && max_tokens > ctas * 2048) ctas *= 2;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int ctas = (max_tokens + pa::SLOT_ROWS_PER_CTA - 1) / pa::SLOT_ROWS_PER_CTA;
+  if (ctas > pa::SLOT_MAX_CTAS) {  // on 264,000 rows: 8.5 us as two launches over the GPU, 55 us as one cluster
+    ctas = max_tokens / 1024 < di.num_sms ? max_tokens / 1024 : di.num_sms;
+    pa::slots_kernel<1024><<<ctas, 1024, 0, st>>>(p, pa::SLOTS_ROWS);
+    const int r = pa::check_launch(cudaSuccess, "slots_kernel launch");
+    if (r != PA_OK) return r;
+    pa::slots_kernel<1024><<<1, 1024, 0, st>>>(p, pa::SLOTS_STATE);
+    return pa::check_launch(cudaSuccess, "slots_kernel launch");
+  }
+  if (ctas < 1) ctas = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(pa::SLOT_THREADS);
-  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
@@ -318,5 +336,10 @@ extern "C" int pa_step_slots(const int32_t* new_tokens, const int32_t* context_l
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return pa::check_launch(cudaLaunchKernelEx(&cfg, pa::slots_kernel, p), "slots_kernel launch");
+  const int parts = pa::SLOTS_ROWS | pa::SLOTS_STATE;
+  // a small batch: fewer warps to wait for at each of the scan's barriers
+  const bool small = num_seqs <= 256 && max_tokens <= 1024;
+  cfg.blockDim = dim3(small ? 256 : 1024);
+  return pa::check_launch(cudaLaunchKernelEx(&cfg, small ? pa::slots_kernel<256> : pa::slots_kernel<1024>, p, parts),
+                          "slots_kernel launch");
 }
