@@ -27,6 +27,7 @@ namespace pa {
 namespace {
 
 constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_MAX_TOKENS = 8;  // a CTA's
 
 struct RopeParams {
   __nv_bfloat16* q_out;        // [T, Hq, D]; heads counted first: 0 .. Hq-1 are q, then k, then v
@@ -48,25 +49,33 @@ struct RopeParams {
 enum Cache { CACHE_BF16, CACHE_E4M3, CACHE_INT4 };
 enum Pairs { PAIRS_NONE, PAIRS_HALF, PAIRS_INTERLEAVED };
 
-// a c - b s (b's term added for the second half of a pair), rounded once to
-// bf16.  Two fused operations leave an error of at most 2 ulp of binary32; only
-// a value that close to a bf16 tie is taken again in binary64, where both
-// products are exact.
-__device__ __noinline__ uint32_t turn_exact(float a, float c, float b, float s) {
+// Eight values a c + b s, each rounded once to bf16.  Two fused operations (the product's error added to the sum) leave
+// an error of at most 1.5 ulp of binary32, which decides the rounding only within 2 ulp of a tie; such a value, and an
+// infinity or NaN, is taken again in binary64, where both products are exact.  One vector in 1600 holds one.
+__device__ __noinline__ float turn_exact(float a, float c, float b, float s) {
   const double d = static_cast<double>(a) * c + static_cast<double>(b) * s;
   const float z = __double2float_rz(d);  // round to odd: then one more rounding is right
-  uint32_t u = __float_as_uint(z);
-  if (static_cast<double>(z) != d) u |= 1;
-  return u;
+  return static_cast<double>(z) != d ? __uint_as_float(__float_as_uint(z) | 1) : z;
 }
-__device__ __forceinline__ uint32_t turn(float a, float c, float b, float s) {
-  const float p = b * s;
-  const float e = fmaf(b, s, -p);
-  float r = fmaf(a, c, p) + e;
-  if (r != r) r = fmaf(a, c, p);  // an infinite product has no rest to add
-  uint32_t u = __float_as_uint(r);
-  if (((u + 4u) & 0xffffu) - 0x8000u <= 8u) u = turn_exact(a, c, b, s);
-  return __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(u)));
+__device__ __forceinline__ uint4 turn(const float (&a)[8], const float (&b)[8], const float (&c)[8],
+                                      const float (&s)[8]) {
+  float r[8], finite = 0.f;
+  uint32_t tie = 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float p = b[i] * s[i];
+    const float e = fmaf(b[i], s[i], -p);
+    r[i] = fmaf(a[i], c[i], p) + e;
+    finite = fmaf(r[i], 0.f, finite);                                   // NaN if r is not finite
+    tie = min(tie, __float_as_uint(r[i]) * 65536u + 0x80020000u);       // the low half, with ties moved to 0 .. 4
+  }
+  if (tie < 0x00050000u || finite != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (__float_as_uint(r[i]) * 65536u + 0x80020000u < 0x00050000u || r[i] * 0.f != 0.f)
+        r[i] = turn_exact(a[i], c[i], b[i], s[i]);
+  }
+  return make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7]));
 }
 
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
@@ -77,13 +86,28 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, float inv) {
 }
 
 // Quantise 32 dims held as 8 by each of 4 adjacent lanes (j = lane & 3) and
-// store them: lane j writes the chunk's j-th 4 bytes, lane 0 its scale.
+// store them (all lanes of the warp call): lane j writes the chunk's j-th 4 bytes, lane 0 its scale.  Codes
+// come from x * (1 / s), which tells every rounding but those next to a tie;
+// those are told by the exact rest x - n s.  A chunk with an odd scale (zero,
+// subnormal, clamped, NaN) is divided.
 template <int D>
 __device__ __forceinline__ void store_int4(uint8_t* record, int block_size, int row, int chunk, int j, uint4 x,
-                                           unsigned group) {
+                                           bool store) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float f[8], m = 0.f;
-  bool nan = false;
+  // bf16 magnitudes order as integers, NaN above infinity above all
+  uint32_t m2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+  m2 = __vmaxu2(m2, __shfl_xor_sync(FULL_MASK, m2, 1));
+  m2 = __vmaxu2(m2, __shfl_xor_sync(FULL_MASK, m2, 2));
+  const uint32_t top_bits = max(m2 & 0xffffu, m2 >> 16);
+  const float m = fminf(__uint_as_float(top_bits << 16), 458528.f);  // 7 * 65504, the largest scale's
+  // m / 7 rounded to nearest: the quotient by the rounded reciprocal, corrected by its exact residual
+  float top = m * 0.142857149243354797f;
+  top = fmaf(fmaf(-7.f, top, m), 0.142857149243354797f, top);
+  const __half h = top_bits > 0x7f80u ? __ushort_as_half(0x7fff) : __float2half_rn(top);
+  const float s = __half2float(h);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  float f[8], n[8], far = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f[2 * i] = lo_f32(w[i]);
@@ -91,177 +115,205 @@ __device__ __forceinline__ void store_int4(uint8_t* record, int block_size, int 
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    m = fmaxf(m, fabsf(f[i]));
-    nan |= f[i] != f[i];
+    n[i] = fmaf(f[i], inv, 12582912.f);  // 1.5 2^23: the nearest integer, ties to even, in the low bits
+    far = fmaxf(far, fabsf(fmaf(f[i], inv, 12582912.f - n[i])));
   }
-  if (nan) m = __uint_as_float(0x7fffffffu);
+  if (!(s >= 6.2e-5f) || top_bits > 0x48e0u) {  // (0x48e0: 458752, where the scale is clamped)
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {  // a NaN wins: the chunk then reads as NaN
-    const float y = __shfl_xor_sync(group, m, o);
-    m = (m != m || y != y) ? __uint_as_float(0x7fffffffu) : fmaxf(m, y);
+    for (int i = 0; i < 8; ++i) {
+      const float t = s > 0.f ? rintf(__fdiv_rn(f[i], s)) : 0.f;
+      n[i] = fminf(fmaxf(t, -7.f), 7.f) + 12582912.f;
+    }
+  } else if (far > 0.49999f) {  // next to a tie (one chunk in 35: bf16 values over a scale of few bits): by the exact rest
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float k = n[i] - 12582912.f;
+      const float rest = fmaf(-k, s, f[i]), twice = fabsf(rest + rest);
+      if (twice > s || (twice == s && (__float_as_uint(n[i]) & 1))) n[i] += copysignf(1.f, rest);
+    }
   }
-  const float top = __fdiv_rn(m, 7.0f);
-  const __half h = __float2half_rn(top > 65504.f ? 65504.f : top);
-  const float s = __half2float(h);
   uint32_t out[4];
+  const uint32_t place = 1u << (4 * j);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t v = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float n = s > 0.f ? rintf(__fdiv_rn(f[2 * i + k], s)) : 0.f;
-      n = fminf(fmaxf(n, -7.f), 7.f);
-      v |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (16 * k + 4 * j);
-    }
-    out[i] = v;
+    const uint32_t pair = __byte_perm(__float_as_uint(n[2 * i]), __float_as_uint(n[2 * i + 1]), 0x5410);
+    out[i] = ((pair & 0x000f000fu) ^ 0x00080008u) * place;  // n + 8
   }
   // unit 2 i + k has this lane's nibble j of dim 8 j + 2 i + k: gather the four lanes' nibbles
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    out[i] |= __shfl_xor_sync(group, out[i], 1);
-    out[i] |= __shfl_xor_sync(group, out[i], 2);
+    out[i] |= __shfl_xor_sync(FULL_MASK, out[i], 1);
+    out[i] |= __shfl_xor_sync(FULL_MASK, out[i], 2);
   }
   const uint32_t mine = j == 0 ? out[0] : j == 1 ? out[1] : j == 2 ? out[2] : out[3];
+  if (!store) return;
   *reinterpret_cast<uint32_t*>(record + int4_code_offset<D>(row, chunk) + 4 * j) = mine;
   if (j == 0) *reinterpret_cast<__half*>(record + int4_scale_offset<D>(block_size, row, chunk)) = h;
 }
 
 template <int D, Cache CACHE, Pairs PAIRS>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const RopeParams p, int tokens) {
   constexpr int VECS = D / 8;                       // 8 .. 32: a head's vectors lie in one warp
   constexpr int HEADS = ROPE_THREADS / VECS;        // heads a CTA takes at a time
+  __shared__ int sh_pos[ROPE_MAX_TOKENS];           // -1: nothing of the row is written
+  __shared__ long long sh_slot[ROPE_MAX_TOKENS];    // -1: not stored
+  __shared__ float4 sh_row[PAIRS == PAIRS_NONE ? 1 : ROPE_MAX_TOKENS * D / 4];
   grid_launch_dependents();
   const int vec = threadIdx.x % VECS;
-  const int h0 = blockIdx.y * HEADS + threadIdx.x / VECS;
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
+  const int h = blockIdx.y * HEADS + threadIdx.x / VECS;  // this thread's head: of q, then of k, then of v
+  const bool some = h < p.num_q_heads + 2 * p.num_kv_heads;
+  const bool is_q = h < p.num_q_heads, is_v = h >= p.num_q_heads + p.num_kv_heads;
+  const int kh = is_q ? 0 : is_v ? h - p.num_q_heads - p.num_kv_heads : h - p.num_q_heads;
   const int bs = 1 << p.block_shift;
-  const unsigned group = 0xfu << (threadIdx.x & 28);
-  const unsigned head_lanes = VECS == 32 ? FULL_MASK : ((1u << (VECS & 31)) - 1) << (threadIdx.x & 31 & ~(VECS - 1));
   const int half_vecs = p.rot_dim / 16;
   const bool turns = PAIRS != PAIRS_NONE && vec * 8 < p.rot_dim;
-  for (int t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
+  const bool second = vec >= half_vecs;
+  const int other = second ? vec - half_vecs : vec + half_vecs;
+  const int partner = (threadIdx.x & 31) - vec % 32 + other;  // lane of the pair's other vector
+  const int pair = second ? vec - half_vecs : vec;            // the vector's place in the table's half row
+  const int t0 = blockIdx.x * tokens;
+  const int n = min(tokens, p.num_tokens - t0);
+
+  // The thread walks over the tokens; the vectors of the next two are on their way.
+  const long long stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
+  const __nv_bfloat16* src = (is_q ? p.q + static_cast<long long>(h) * D
+                              : is_v ? p.v_new + static_cast<long long>(kh) * D
+                                     : p.k_new + static_cast<long long>(kh) * D) + t0 * stride + vec * 8;
+  const auto fetch = [&](int i) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (some && i < n) v = *reinterpret_cast<const uint4*>(src);
+    src += stride;
+    return v;
+  };
+  uint4 x0 = fetch(0), x1 = fetch(1);
+  __nv_bfloat16* dst = p.q_out + (static_cast<long long>(t0) * p.num_q_heads + h) * D + vec * 8;
+  const long long dst_step = static_cast<long long>(p.num_q_heads) * D;
+  void* cache = is_v ? p.v_cache : p.k_cache;
+
+  // the tokens' slots, positions and table rows
+  if (threadIdx.x < n) {
+    const int t = t0 + threadIdx.x;
     long long slot = p.slots[t];
-    if (slot >= p.num_slots) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
+    int pos = PAIRS == PAIRS_NONE ? 0 : p.positions[t], bits = 0;
+    if (PAIRS != PAIRS_NONE && pos >= p.table_len) {
+      bits = PA_STATUS_BIT(PA_ERR_RANGE);
+      pos = -1;
+    }
+    if (pos >= 0 && slot >= p.num_slots) {
+      bits = PA_STATUS_BIT(PA_ERR_RANGE);
       slot = -1;
     }
-    float c[8], s[8];
-    if (PAIRS != PAIRS_NONE) {
-      const int pos = p.positions[t];
-      if (pos < 0) continue;  // padding: nothing of this row is written
-      if (pos >= p.table_len) {
-        if (threadIdx.x == 0 && blockIdx.y == 0) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
-        continue;
-      }
-      if (turns) {
-        const float* row = p.table + static_cast<long long>(pos) * p.rot_dim;
-        if (PAIRS == PAIRS_HALF) {
-          const bool second = vec >= half_vecs;
-          const int i = (second ? vec - half_vecs : vec) * 8;
-#pragma unroll
-          for (int k = 0; k < 8; k += 4) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(row + i + k));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(row + p.rot_dim / 2 + i + k));
-            c[k] = a.x, c[k + 1] = a.y, c[k + 2] = a.z, c[k + 3] = a.w;
-            s[k] = b.x, s[k + 1] = b.y, s[k + 2] = b.z, s[k + 3] = b.w;
-          }
-          if (!second) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] = -s[k];
-          }
-        } else {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(row + vec * 4));
-          const float4 b = __ldg(reinterpret_cast<const float4*>(row + p.rot_dim / 2 + vec * 4));
-          c[0] = c[1] = a.x, c[2] = c[3] = a.y, c[4] = c[5] = a.z, c[6] = c[7] = a.w;
-          s[0] = -b.x, s[1] = b.x, s[2] = -b.y, s[3] = b.y, s[4] = -b.z, s[5] = b.z, s[6] = -b.w, s[7] = b.w;
-        }
-      }
+    if (bits && blockIdx.y == 0) set_status(p.status, bits);
+    sh_pos[threadIdx.x] = pos < 0 ? -1 : pos;
+    sh_slot[threadIdx.x] = slot < 0 ? -1 : slot;
+  }
+  __syncthreads();
+  if (PAIRS != PAIRS_NONE) {
+    const int words = p.rot_dim / 4;  // of a table row, by 16 bytes
+    for (int t = threadIdx.x / 32; t < n; t += ROPE_THREADS / 32) {
+      const int pos = sh_pos[t];
+      if (pos < 0) continue;
+      const float4* row = reinterpret_cast<const float4*>(p.table + static_cast<long long>(pos) * p.rot_dim);
+      for (int w = threadIdx.x & 31; w < words; w += 32) sh_row[t * (D / 4) + w] = __ldg(row + w);
     }
-    const long long blk = slot >> p.block_shift;
-    const int off = static_cast<int>(slot & (bs - 1));
-    for (int h = h0; h < heads; h += gridDim.y * HEADS) {
-      const bool is_q = h < p.num_q_heads;
-      const bool is_v = h >= p.num_q_heads + p.num_kv_heads;
-      const int kh = is_q ? 0 : is_v ? h - p.num_q_heads - p.num_kv_heads : h - p.num_q_heads;
-      const __nv_bfloat16* src = is_q   ? p.q + t * p.q_stride + static_cast<long long>(h) * D
-                                 : is_v ? p.v_new + t * p.v_stride + static_cast<long long>(kh) * D
-                                        : p.k_new + t * p.k_stride + static_cast<long long>(kh) * D;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      const bool live = is_q || slot >= 0;
-      if (live) x = *reinterpret_cast<const uint4*>(src + vec * 8);
-      if (PAIRS != PAIRS_NONE) {
-        uint4 y = x;
-        const bool rotate = turns && !is_v && live;
-        if (PAIRS == PAIRS_HALF && rotate) {
-          const int other = vec >= half_vecs ? vec - half_vecs : vec + half_vecs;
-          y = *reinterpret_cast<const uint4*>(src + other * 8);
-        }
-        __syncwarp(head_lanes);  // both vectors of every pair are loaded before any is stored (q in place)
-        if (rotate) {
-          const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
-          uint32_t o[4];
+    __syncthreads();
+  }
+
+  for (int i = 0; i < n; ++i, dst += dst_step) {
+    const bool mine = some && sh_pos[i] >= 0;
+    uint4 out = x0, y = x0;
+    if (PAIRS == PAIRS_HALF) {
+      y.x = __shfl_sync(FULL_MASK, x0.x, partner);
+      y.y = __shfl_sync(FULL_MASK, x0.y, partner);
+      y.z = __shfl_sync(FULL_MASK, x0.z, partner);
+      y.w = __shfl_sync(FULL_MASK, x0.w, partner);
+    }
+    if (PAIRS != PAIRS_NONE && turns && !is_v && mine) {
+      const uint32_t wa[4] = {x0.x, x0.y, x0.z, x0.w}, wb[4] = {y.x, y.y, y.z, y.w};
+      float a[8], b[8], c[8], s[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float al = lo_f32(a[i]), ah = hi_f32(a[i]);
-            const float bl = PAIRS == PAIRS_HALF ? lo_f32(b[i]) : ah, bh = PAIRS == PAIRS_HALF ? hi_f32(b[i]) : al;
-            o[i] = turn(al, c[2 * i], bl, s[2 * i]) | (turn(ah, c[2 * i + 1], bh, s[2 * i + 1]) << 16);
-          }
-          x = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+      for (int m = 0; m < 4; ++m) {  // b: the partner, its sign turned for the first of a pair
+        const uint32_t w = PAIRS == PAIRS_HALF ? wb[m] ^ (second ? 0u : 0x80008000u)
+                                               : __byte_perm(wa[m], wa[m], 0x1032) ^ 0x00008000u;
+        a[2 * m] = lo_f32(wa[m]);
+        a[2 * m + 1] = hi_f32(wa[m]);
+        b[2 * m] = lo_f32(w);
+        b[2 * m + 1] = hi_f32(w);
       }
-      if (is_q) {
-        *reinterpret_cast<uint4*>(p.q_out + (static_cast<long long>(t) * p.num_q_heads + h) * D + vec * 8) = x;
-      } else if (slot >= 0) {
-        void* cache = is_v ? p.v_cache : p.k_cache;
-        const long long head = blk * p.num_kv_heads + kh;
-        if (CACHE == CACHE_BF16) {
-          static_cast<uint4*>(cache)[(head * bs + off) * VECS + vec] = x;
-        } else if (CACHE == CACHE_E4M3) {
-          const float inv = is_v ? p.v_inv : p.k_inv;
-          static_cast<uint2*>(cache)[(head * bs + off) * VECS + vec] =
-              make_uint2(e4m3_pair(x.x, inv) | (e4m3_pair(x.y, inv) << 16),
-                         e4m3_pair(x.z, inv) | (e4m3_pair(x.w, inv) << 16));
-        } else {
-          store_int4<D>(static_cast<uint8_t*>(cache) + head * int4_record_bytes(bs, D), bs, off, vec >> 2, vec & 3, x,
-                        group);
+      const float4* row = sh_row + i * (D / 4);
+      if (PAIRS == PAIRS_HALF) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float4 cc = row[pair * 2 + k], ss = row[p.rot_dim / 8 + pair * 2 + k];
+          c[4 * k] = cc.x, c[4 * k + 1] = cc.y, c[4 * k + 2] = cc.z, c[4 * k + 3] = cc.w;
+          s[4 * k] = ss.x, s[4 * k + 1] = ss.y, s[4 * k + 2] = ss.z, s[4 * k + 3] = ss.w;
         }
+      } else {
+        const float4 cc = row[vec], ss = row[p.rot_dim / 8 + vec];
+        c[0] = c[1] = cc.x, c[2] = c[3] = cc.y, c[4] = c[5] = cc.z, c[6] = c[7] = cc.w;
+        s[0] = s[1] = ss.x, s[2] = s[3] = ss.y, s[4] = s[5] = ss.z, s[6] = s[7] = ss.w;
       }
+      out = turn(a, b, c, s);
+    }
+    x0 = x1;
+    x1 = fetch(i + 2);  // (q in place: a vector is fetched and stored by its own thread, its pair's came by the exchange)
+    if (mine && is_q) *reinterpret_cast<uint4*>(dst) = out;
+    const long long slot = sh_slot[i];
+    const bool store = mine && !is_q && slot >= 0;
+    const long long head = (slot >> p.block_shift) * p.num_kv_heads + kh;
+    const int off = static_cast<int>(slot & (bs - 1));
+    if (CACHE == CACHE_BF16) {
+      if (store) static_cast<uint4*>(cache)[(head * bs + off) * VECS + vec] = out;
+    } else if (CACHE == CACHE_E4M3) {
+      const float inv = is_v ? p.v_inv : p.k_inv;
+      if (store)
+        static_cast<uint2*>(cache)[(head * bs + off) * VECS + vec] =
+            make_uint2(e4m3_pair(out.x, inv) | (e4m3_pair(out.y, inv) << 16),
+                       e4m3_pair(out.z, inv) | (e4m3_pair(out.w, inv) << 16));
+    } else if (__any_sync(FULL_MASK, store)) {  // whole warps: their lanes exchange codes
+      store_int4<D>(static_cast<uint8_t*>(cache) + head * int4_record_bytes(bs, D), bs, off, vec >> 2, vec & 3, out,
+                    store);
     }
   }
 }
 
-// Rows of the 4-bit cache as values: one thread per 8 dims (k, then v).
+// Rows of the 4-bit cache as values: one thread per 4 dims (k, then v), so that a warp stores whole lines.
 template <int D>
 __global__ void __launch_bounds__(ROPE_THREADS)
     read_int4_kernel(float* k_out, float* v_out, const uint8_t* k_cache, const uint8_t* v_cache, const int32_t* slots,
-                     int num_tokens, int num_kv_heads, int block_shift, long long num_slots, int* status) {
-  constexpr int VECS = D / 8, HEADS = ROPE_THREADS / VECS;
-  const int vec = threadIdx.x % VECS, chunk = vec >> 2, j = vec & 3, bs = 1 << block_shift;
-  for (int t = blockIdx.x; t < num_tokens; t += gridDim.x) {
-    const long long slot = slots[t];
+                     int num_tokens, int num_kv_heads, int block_shift, long long num_slots, int tokens, int* status) {
+  constexpr int VECS = D / 4, HEADS = ROPE_THREADS / VECS;
+  const int vec = threadIdx.x % VECS, chunk = vec >> 3, bs = 1 << block_shift;
+  const int j = vec >> 1 & 3;    // dims 8 j + 4 half .. + 3 of the chunk: nibble j of four units
+  const int half = vec & 1;
+  __shared__ long long sh_slot[ROPE_MAX_TOKENS];
+  const int t0 = blockIdx.x * tokens, n = min(tokens, num_tokens - t0);
+  if (threadIdx.x < n) {
+    const long long slot = slots[t0 + threadIdx.x];
+    if (slot >= num_slots && blockIdx.y == 0) set_status(status, PA_STATUS_BIT(PA_ERR_RANGE));
+    sh_slot[threadIdx.x] = slot < num_slots ? slot : -1;
+  }
+  __syncthreads();
+  const int h = blockIdx.y * HEADS + threadIdx.x / VECS;
+  if (h >= 2 * num_kv_heads) return;
+  const bool is_v = h >= num_kv_heads;
+  const int kh = is_v ? h - num_kv_heads : h;
+  const uint8_t* cache = is_v ? v_cache : k_cache;
+  float4* dst = reinterpret_cast<float4*>((is_v ? v_out : k_out) + (static_cast<long long>(t0) * num_kv_heads + kh) * D) + vec;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const long long slot = sh_slot[i];
     if (slot < 0) continue;
-    if (slot >= num_slots) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) set_status(status, PA_STATUS_BIT(PA_ERR_RANGE));
-      continue;
-    }
-    const long long blk = slot >> block_shift;
     const int off = static_cast<int>(slot & (bs - 1));
-    for (int h = blockIdx.y * HEADS + threadIdx.x / VECS; h < 2 * num_kv_heads; h += gridDim.y * HEADS) {
-      const bool is_v = h >= num_kv_heads;
-      const int kh = is_v ? h - num_kv_heads : h;
-      const uint8_t* rec = (is_v ? v_cache : k_cache) + (blk * num_kv_heads + kh) * int4_record_bytes(bs, D);
-      const uint4 w = *reinterpret_cast<const uint4*>(rec + int4_code_offset<D>(off, chunk));
-      const float s = __half2float(*reinterpret_cast<const __half*>(rec + int4_scale_offset<D>(bs, off, chunk)));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      float f[8];
+    const uint8_t* rec = cache + ((slot >> block_shift) * num_kv_heads + kh) * int4_record_bytes(bs, D);
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(rec + int4_code_offset<D>(off, chunk) + 8 * half));
+    const float s = __half2float(__ldg(reinterpret_cast<const __half*>(rec + int4_scale_offset<D>(bs, off, chunk))));
+    const uint32_t u[2] = {w.x >> (4 * j), w.y >> (4 * j)};
+    float f[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)  // unit i, nibble j: dim 8 j + i
-        f[i] = static_cast<float>(static_cast<int>((u[i >> 1] >> (16 * (i & 1) + 4 * j)) & 15) - 8) * s;
-      float4* dst = reinterpret_cast<float4*>((is_v ? v_out : k_out) +
-                                              (static_cast<long long>(t) * num_kv_heads + kh) * D + vec * 8);
-      dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-      dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
+    for (int k = 0; k < 4; ++k)
+      f[k] = static_cast<float>(static_cast<int>(u[k >> 1] >> (16 * (k & 1)) & 15) - 8) * s;
+    dst[static_cast<long long>(i) * num_kv_heads * VECS] = make_float4(f[0], f[1], f[2], f[3]);
   }
 }
 
@@ -299,21 +351,20 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// CTAs in x walk over tokens, in y over heads: enough of both to fill the GPU, no more passes than needed.
-dim3 row_grid(int num_tokens, int heads, int heads_per_cta, int num_sms) {
-  const int passes = (heads + heads_per_cta - 1) / heads_per_cta;
-  const long long want = static_cast<long long>(num_sms) * 8;
-  long long y = (want + num_tokens - 1) / num_tokens;
-  if (y > passes) y = passes;
-  long long x = num_tokens < 65535ll * 16 ? num_tokens : 65535ll * 16;
-  return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
+// x: runs of tokens, y: heads.  A CTA's slots, positions and table rows are fetched once, then its tokens stream: as
+// many as leave the GPU four CTAs an SM.
+dim3 row_grid(int num_tokens, int heads, int heads_per_cta, int num_sms, int* tokens) {
+  const int y = (heads + heads_per_cta - 1) / heads_per_cta;
+  const long long n = static_cast<long long>(num_tokens) * y / (num_sms * 4ll);
+  *tokens = static_cast<int>(n < 1 ? 1 : n > ROPE_MAX_TOKENS ? ROPE_MAX_TOKENS : n);
+  return dim3(static_cast<unsigned>((num_tokens + *tokens - 1) / *tokens), static_cast<unsigned>(y));
 }
 
 template <int D, Cache CACHE, Pairs PAIRS>
 int launch_rope(const RopeParams& p, cudaStream_t stream, int num_sms) {
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
-  rope_kernel<D, CACHE, PAIRS><<<row_grid(p.num_tokens, heads, ROPE_THREADS / (D / 8), num_sms), ROPE_THREADS, 0,
-                                stream>>>(p);
+  int tokens;
+  const dim3 grid = row_grid(p.num_tokens, p.num_q_heads + 2 * p.num_kv_heads, ROPE_THREADS / (D / 8), num_sms, &tokens);
+  rope_kernel<D, CACHE, PAIRS><<<grid, ROPE_THREADS, 0, stream>>>(p, tokens);
   return check_launch(cudaSuccess, "rope_kernel launch");
 }
 
@@ -516,13 +567,14 @@ int pa_cache_read_int4(float* k_out, float* v_out, const void* k_cache, const vo
   if (rc != PA_OK) return rc;
   const long long slots = static_cast<long long>(num_blocks) * block_size;
   const int shift = block_size == 16 ? 4 : 5;
-  const dim3 grid = pa::row_grid(num_tokens, 2 * num_kv_heads, pa::ROPE_THREADS / (head_dim / 8), di.num_sms);
+  int tokens;
+  const dim3 grid = pa::row_grid(num_tokens, 2 * num_kv_heads, pa::ROPE_THREADS / (head_dim / 4), di.num_sms, &tokens);
   const auto kernel = head_dim == 64    ? pa::read_int4_kernel<64>
                       : head_dim == 128 ? pa::read_int4_kernel<128>
                                         : pa::read_int4_kernel<256>;
   kernel<<<grid, pa::ROPE_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
       k_out, v_out, static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), slot_mapping,
-      num_tokens, num_kv_heads, shift, slots, dev_status);
+      num_tokens, num_kv_heads, shift, slots, tokens, dev_status);
   return pa::check_launch(cudaSuccess, "read_int4_kernel launch");
 }
 
