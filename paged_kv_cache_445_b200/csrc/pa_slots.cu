@@ -16,7 +16,8 @@
 // of the rows, found by binary search in the tile's row ends.  The lengths and
 // the queue state may be updated in place, so they are written only when every
 // CTA has read them: after the barrier of one cluster of up to 8 CTAs, or, for
-// row buffers that keep more CTAs busy, by a second launch.
+// row buffers that keep more CTAs busy, by a second launch.  Written elsewhere,
+// they need neither.
 #include <cooperative_groups.h>
 
 #include "pa_device.cuh"
@@ -31,7 +32,9 @@ namespace cg = cooperative_groups;
 constexpr int SLOT_MAX_CTAS = 8;        // of a cluster
 constexpr int SLOT_ROWS_PER_CTA = 2048;  // below that a second CTA only repeats the scan
 
-enum SlotsPart { SLOTS_ROWS = 1, SLOTS_STATE = 2 };  // what a launch writes
+// What a launch writes; APART: the lengths and the queue state go elsewhere than they came from, so nothing is waited
+// for before they are written.
+enum SlotsPart { SLOTS_ROWS = 1, SLOTS_STATE = 2, SLOTS_APART = 4 };
 
 struct SlotsParams {
   const int32_t* new_tokens;
@@ -81,6 +84,15 @@ __device__ __forceinline__ long long warp_inclusive(long long v, int lane) {
   return v;
 }
 
+// Sum of the totals of the warps before this one, and of all WARPS: every warp scans them itself.
+template <int WARPS>
+__device__ __forceinline__ long long before_warp(const long long* totals, int warp, int lane, long long& all) {
+  const long long incl = warp_inclusive(lane < WARPS ? totals[lane] : 0, lane);
+  all = __shfl_sync(FULL_MASK, incl, 31);
+  const long long x = __shfl_sync(FULL_MASK, incl, warp > 0 ? warp - 1 : 0);
+  return warp > 0 ? x : 0;
+}
+
 // Load sequence s of the tile and scan the tile; `carry` moves to its end.
 template <int THREADS>
 __device__ Seq scan_tile(const SlotsParams& p, SlotsShared<THREADS>& sh, int s, int count, bool bad_queue, Carry& carry) {
@@ -112,13 +124,8 @@ __device__ Seq scan_tile(const SlotsParams& p, SlotsShared<THREADS>& sh, int s, 
   long long v = warp_inclusive(q.n > 0 ? q.n : 0, lane);
   if (lane == 31) sh.warp[0][warp] = v;
   __syncthreads();
-  long long base = carry.rows, total = 0;
-#pragma unroll 8
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const long long x = sh.warp[0][w];
-    base += w < warp ? x : 0;
-    total += x;
-  }
+  long long total;
+  const long long base = carry.rows + before_warp<THREADS / 32>(sh.warp[0], warp, lane, total);
   q.rows_end = base + v;
   carry.rows += total;
   if (fits && q.rows_end > p.max_tokens) {
@@ -133,15 +140,9 @@ __device__ Seq scan_tile(const SlotsParams& p, SlotsShared<THREADS>& sh, int s, 
     sh.warp[2][warp] = bv;
   }
   __syncthreads();
-  long long nb = carry.need, nt = 0, bb = carry.back, bt = 0;
-#pragma unroll 8
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const long long x = sh.warp[1][w], y = sh.warp[2][w];
-    nb += w < warp ? x : 0;
-    nt += x;
-    bb += w < warp ? y : 0;
-    bt += y;
-  }
+  long long nt, bt;
+  const long long nb = carry.need + before_warp<THREADS / 32>(sh.warp[1], warp, lane, nt);
+  const long long bb = carry.back + before_warp<THREADS / 32>(sh.warp[2], warp, lane, bt);
   q.need_end = nb + nv;
   q.back_end = bb + bv;
   carry.need += nt;
@@ -255,8 +256,10 @@ __global__ void __launch_bounds__(THREADS) slots_kernel(const SlotsParams p, int
   if (!(parts & SLOTS_STATE)) return;
   // every CTA has read the lengths and the queue state: now they may change
   if (parts & SLOTS_ROWS) {
-    __threadfence();
-    cg::this_cluster().sync();
+    if (!(parts & SLOTS_APART)) {
+      __threadfence();
+      cg::this_cluster().sync();
+    }
     if (rank != 0) return;
   }
   if (tiles == 1 && (parts & SLOTS_ROWS)) {
@@ -317,11 +320,13 @@ extern "C" int pa_step_slots(const int32_t* new_tokens, const int32_t* context_l
                     num_seqs,       max_blocks_per_seq, num_blocks, block_size == 16 ? 4 : 5, max_tokens, dev_status};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int ctas = (max_tokens + pa::SLOT_ROWS_PER_CTA - 1) / pa::SLOT_ROWS_PER_CTA;
-  if (ctas > pa::SLOT_MAX_CTAS) {  // on 264,000 rows: 8.5 us as two launches over the GPU, 55 us as one cluster
+  const bool apart = context_lens_out != context_lens && blocks_held_out != blocks_held && free_state_out != free_state;
+  if (ctas > pa::SLOT_MAX_CTAS) {  // 264,000 rows: 55 us as one cluster, 18 as two launches over the GPU, 16 as one
     ctas = max_tokens / 1024 < di.num_sms ? max_tokens / 1024 : di.num_sms;
-    pa::slots_kernel<1024><<<ctas, 1024, 0, st>>>(p, pa::SLOTS_ROWS);
+    const int rows = pa::SLOTS_ROWS | (apart ? pa::SLOTS_STATE | pa::SLOTS_APART : 0);
+    pa::slots_kernel<1024><<<ctas, 1024, 0, st>>>(p, rows);
     const int r = pa::check_launch(cudaSuccess, "slots_kernel launch");
-    if (r != PA_OK) return r;
+    if (r != PA_OK || apart) return r;
     pa::slots_kernel<1024><<<1, 1024, 0, st>>>(p, pa::SLOTS_STATE);
     return pa::check_launch(cudaSuccess, "slots_kernel launch");
   }
@@ -336,7 +341,7 @@ extern "C" int pa_step_slots(const int32_t* new_tokens, const int32_t* context_l
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const int parts = pa::SLOTS_ROWS | pa::SLOTS_STATE;
+  const int parts = pa::SLOTS_ROWS | pa::SLOTS_STATE | (apart ? pa::SLOTS_APART : 0);
   // a small batch: fewer warps to wait for at each of the scan's barriers
   const bool small = num_seqs <= 256 && max_tokens <= 1024;
   cfg.blockDim = dim3(small ? 256 : 1024);
