@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   __shared__ long long scan[WARPS];
   __shared__ WarpEnd ends[WARPS];
   __shared__ WarpState walks[WARPS];
-  __shared__ int sh_merge;
+  __shared__ int sh_merge[2];
   __shared__ int arrived[WARPS];  // pieces of the item inside the CTA that starts in each warp
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL_MASK, tid >> 5, 0);  // (one value to the compiler)
   const int g = lane >> 2, qd = lane & 3;
@@ -1028,27 +1028,34 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
   // ---- pieces of items that cross CTAs: count them in; the last CTA merges
   __threadfence();
   __syncthreads();
+  int from[2], count[2];
+#pragma unroll
   for (int e = 0; e <= 1; ++e) {
-    const int src = chain[e];
-    if (src < 0) continue;
-    const WarpEnd& we = ends[src];
-    const long long first = we.first[e], after = first + we.units[e];
-    const int f = cta_of(first), t = cta_of(after - 1);
-    const int n = t - f + 1;
-    if (tid == 0) {
-      const int got = atomicAdd(p.counters + f, 1);
-      sh_merge = got == n - 1;
-      if (got == n - 1) p.counters[f] = 0;
-      __threadfence();
+    from[e] = count[e] = 0;
+    if (chain[e] < 0) continue;
+    const WarpEnd& we = ends[chain[e]];
+    from[e] = cta_of(we.first[e]);
+    count[e] = cta_of(we.first[e] + we.units[e] - 1) - from[e] + 1;
+  }
+  if (tid < 2) {  // both at once: neither item waits for the other's merge
+    const int f = tid ? from[1] : from[0], n = tid ? count[1] : count[0];
+    bool last = false;
+    if (n > 0) {
+      last = atomicAdd(p.counters + f, 1) == n - 1;
+      if (last) p.counters[f] = 0;
     }
-    __syncthreads();
-    if (sh_merge) {
-      __nv_bfloat16* out = p.out + (static_cast<long long>(we.row[e]) * p.num_q_heads + we.h[e] * p.group) * D;
-      for (int k = warp; k < NC; k += WARPS)
-        merge_ctas<D, NT>(p.cta_pieces + (static_cast<long long>(f) * 2 + 1) * C::PIECE, n, k, out, p.num_q_heads, p.group,
-                          we.rows[e]);
-    }
-    __syncthreads();
+    sh_merge[tid] = last;
+    __threadfence();
+  }
+  __syncthreads();
+  for (int job = warp; job < 2 * NC; job += WARPS) {
+    const int e = job >= NC, k = job - e * NC;
+    if (!sh_merge[e]) continue;
+    const WarpEnd& we = ends[e ? chain[1] : chain[0]];
+    merge_ctas<D, NT>(p.cta_pieces + (static_cast<long long>(e ? from[1] : from[0]) * 2 + 1) * C::PIECE,
+                      e ? count[1] : count[0], k,
+                      p.out + (static_cast<long long>(we.row[e]) * p.num_q_heads + we.h[e] * p.group) * D, p.num_q_heads,
+                      p.group, we.rows[e]);
   }
 }
 
