@@ -10,12 +10,15 @@
 // whatever the order of operations: codes of a quantised cache taken from it
 // then do not depend on rounding noise.
 //
-// HBM-bound: q is read and written, k and v are read, their cache rows
-// written.  One thread per 16-byte vector (8 dims) of a head; a thread keeps
-// its vector's place in the head and walks over heads, so that a position's
-// table row is read once per thread and not once per head.  The partner vector
-// of a half-split pair is loaded too (an L1 hit); both lie in one warp, which
-// loads before it stores, so q may be rotated in place.
+// Floor: q is read and written, k and v are read, their cache rows written (177 MB
+// for 8192 tokens of 32 + 8 + 8 heads into 4 bits, 27 us).  Instructions bound it:
+// 62 us there, at some 200 a warp and 16-byte vector, most of them the two products
+// rounded once; 4.3 us for 128 decode rows, one chain of dependent loads.
+// One thread takes one 16-byte vector (8 dims) of one head over a run of tokens:
+// its addresses grow by constants, the next two tokens' vectors are in flight, and
+// the tokens' slots, positions and table rows are fetched once per CTA into shared
+// memory.  The other vector of a half-split pair comes from its lane (both lie in
+// one warp, loaded before either is stored, so q may be rotated in place).
 #include <cmath>
 
 #include "pa_device.cuh"
