@@ -12,7 +12,7 @@
 //
 // Floor: q is read and written, k and v are read, their cache rows written (177 MB
 // for 8192 tokens of 32 + 8 + 8 heads into 4 bits, 27 us).  Instructions bound it:
-// 62 us there, at some 200 a warp and 16-byte vector, most of them the two products
+// 64 us there, at some 200 a warp and 16-byte vector, most of them the two products
 // rounded once; 4.3 us for 128 decode rows, one chain of dependent loads.
 // One thread takes one 16-byte vector (8 dims) of one head over a run of tokens:
 // its addresses grow by constants, the next two tokens' vectors are in flight, and
