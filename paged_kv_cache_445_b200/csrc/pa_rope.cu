@@ -447,7 +447,7 @@ int pa_rope_table(float* table, int table_len, int rot_dim, double base, const p
   if (sc.type < PA_ROPE_PLAIN || sc.type > PA_ROPE_BANDS) return PA_ERR_UNSUPPORTED;
   if (sc.type != PA_ROPE_PLAIN && (!(sc.factor > 0.0) || !(sc.factor < INFINITY))) return PA_ERR_SHAPE;
   if ((sc.type == PA_ROPE_YARN || sc.type == PA_ROPE_BANDS) &&
-      (sc.original_positions <= 0 || !(sc.low > 0.0) || !(sc.high > sc.low)))
+      (sc.original_positions <= 0 || !(sc.low > 0.0) || !(sc.high > sc.low) || !(sc.high < INFINITY)))
     return PA_ERR_SHAPE;
   if (!(sc.attention_factor >= 0.0) || !(sc.attention_factor < INFINITY)) return PA_ERR_SHAPE;
   if (sc.type == PA_ROPE_YARN && !(base > 1.0)) return PA_ERR_SHAPE;  // the ramp divides by log(base)

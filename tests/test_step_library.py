@@ -117,3 +117,11 @@ def test_the_binding_checks_its_tensors():
         b.pa_cache_read_int4(t, t, t, t, t)
     with pytest.raises(b.PAError):
         b.pa_int4_workspace_bytes(8, 2, 96)
+
+
+def test_rope_table_refuses_bounds_without_end():
+    inf, nan = float("inf"), float("nan")
+    for type in (3, 4):
+        for low, high in ((1.0, inf), (1.0, nan), (nan, 32.0), (inf, inf)):
+            sc = b.RopeScaling(type, 4096, 2.0, low, high, 0.0)
+            assert L.pa_rope_table(F, 10, 64, 10000.0, ctypes.byref(sc), None) == b.PA_ERR_SHAPE, (type, low, high)
