@@ -332,7 +332,7 @@ struct Frequencies {
 };
 __global__ void __launch_bounds__(256)
     rope_table_kernel(float* table, int table_len, int half, double factor, const __grid_constant__ Frequencies f) {
-  const long long runs = (table_len + ROPE_RUN - 1) / ROPE_RUN;
+  const long long runs = (static_cast<long long>(table_len) + ROPE_RUN - 1) / ROPE_RUN;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < runs * half; i += gridDim.x * 256ll) {
     const long long r = i / half;
     const int k = static_cast<int>(i - r * half);

@@ -320,7 +320,7 @@ extern "C" int pa_step_slots(const int32_t* new_tokens, const int32_t* context_l
                     free_blocks,    free_state,   free_state_out, query_start,   positions,       slot_mapping,
                     num_seqs,       max_blocks_per_seq, num_blocks, block_size == 16 ? 4 : 5, max_tokens, dev_status};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int ctas = (max_tokens + pa::SLOT_ROWS_PER_CTA - 1) / pa::SLOT_ROWS_PER_CTA;
+  int ctas = static_cast<int>((static_cast<long long>(max_tokens) + pa::SLOT_ROWS_PER_CTA - 1) / pa::SLOT_ROWS_PER_CTA);
   const bool apart = context_lens_out != context_lens && blocks_held_out != blocks_held && free_state_out != free_state;
   if (ctas > pa::SLOT_MAX_CTAS) {  // 264,000 rows: 55 us as one cluster, 18 as two launches over the GPU, 16 as one
     ctas = max_tokens / 1024 < di.num_sms ? max_tokens / 1024 : di.num_sms;
