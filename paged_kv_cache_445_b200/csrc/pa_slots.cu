@@ -254,13 +254,13 @@ __global__ void __launch_bounds__(THREADS) slots_kernel(const SlotsParams p, int
       p.slots[t] = -1;
     }
   }
+  // An attention kernel launched behind this one reads offsets and lengths in its prologue, once every CTA here has
+  // ended but before it waits for their stores: every path fences what it wrote (CTA 0 with outputs apart at its end).
+  if (rank != 0 || (parts & SLOTS_STATE) == 0 || (parts & SLOTS_APART) == 0) __threadfence();
   if (!(parts & SLOTS_STATE)) return;
   // every CTA has read the lengths and the queue state: now they may change
   if (parts & SLOTS_ROWS) {
-    if (!(parts & SLOTS_APART)) {
-      __threadfence();
-      cg::this_cluster().sync();
-    }
+    if (!(parts & SLOTS_APART)) cg::this_cluster().sync();
     if (rank != 0) return;
   }
   if (tiles == 1 && (parts & SLOTS_ROWS)) {
@@ -290,8 +290,7 @@ __global__ void __launch_bounds__(THREADS) slots_kernel(const SlotsParams p, int
       p.free_state_out[1] = p.free_state[1];
     }
   }
-  // An attention kernel launched behind this one reads the lengths in its prologue, once every CTA here has ended.
-  __threadfence();
+  __threadfence();  // (as above)
 }
 
 }  // namespace
