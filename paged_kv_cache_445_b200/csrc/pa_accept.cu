@@ -116,18 +116,13 @@ __global__ void __launch_bounds__(ACC_THREADS, 2) accept_kernel(const AcceptPara
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int start = p.query_start[s], end = p.query_start[s + 1];
   const int rows = end - start;
-  if (start < 0 || end < start || end > p.total_rows) {  // uniform over the cluster: all its CTAs leave
+  const bool bad = start < 0 || end < start || end > p.total_rows;
+  if (bad || rows == 0) {  // uniform over the cluster: all its CTAs leave
     if (rank == 0 && tid == 0) {
-      set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
+      if (bad) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
       p.num_accepted[s] = 0;
       if (p.context_lens) p.context_lens_out[s] = p.context_lens[s];
-    }
-    return;
-  }
-  if (rows == 0) {
-    if (rank == 0 && tid == 0) {
-      p.num_accepted[s] = 0;
-      if (p.context_lens) p.context_lens_out[s] = p.context_lens[s];
+      __threadfence();  // an attention kernel launched behind this one reads the lengths in its prologue
     }
     return;
   }
@@ -241,7 +236,7 @@ __global__ void __launch_bounds__(ACC_THREADS, 2) accept_kernel(const AcceptPara
     if (tid == 0) {
       p.num_accepted[s] = acc;
       if (p.context_lens) p.context_lens_out[s] = p.context_lens[s] - (rows - 1 - acc);
-      __threadfence();  // an attention kernel launched behind this one reads the lengths in its prologue
+      __threadfence();  // (as above)
     }
   }
   if (owner < 0) {  // u times the total is not passed (rounding, u >= 1): the last token with a weight

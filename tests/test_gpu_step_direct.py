@@ -58,3 +58,44 @@ def test_varlen_attention_behind_the_slots(b):
         assert int(status.item()) == 0
         assert all(torch.equal(x, y) for x, y in zip(*results)), i
         assert int(results[0][1][-1]) == int(new.sum()) and torch.equal(results[0][2], ctx_in + new)
+
+
+def test_decode_behind_the_verification():
+    """Sequences with no rows, with bad offsets and with refused drafts write their lengths on three paths."""
+    import paged_kv_cache_445_b200 as pa
+    rng = np.random.default_rng(7)
+    b, bs, width, hq, hkv, d, vocab = 96, 16, 8, 8, 2, 128, 300
+    nb = b * width
+    kc, vc, q = rand(rng, nb, hkv, bs, d), rand(rng, nb, hkv, bs, d), rand(rng, b, hq, d)
+    tables = i32(rng.permutation(nb).reshape(b, width))
+    rows = np.where(np.arange(b) % 3 == 0, 0, rng.integers(1, 5, b))
+    start = np.concatenate([[0], np.cumsum(rows)])
+    t = int(start[-1])
+    start[-1] += 5  # the last sequence's rows end past the buffer: it keeps its length, with the RANGE bit
+    ctx = rng.integers(10, width * bs, b)
+    target, draft = (torch.from_numpy(rng.random((t, vocab)).astype(np.float32)).cuda() for _ in range(2))
+    tokens, uniforms = i32(rng.integers(0, vocab, t)), torch.from_numpy(rng.random(t).astype(np.float32)).cuda()
+    ctx_in, qs = i32(ctx), i32(start)
+    ctx_out, accepted = torch.zeros_like(ctx_in), torch.zeros_like(ctx_in)
+    out_tokens = torch.zeros(t, dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(q)
+    ws = pa.make_workspace(b, hq, hkv, d, width, bs)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for i in range(12):
+        results = []
+        for wait in (True, False):
+            for x in (ctx_out, out):
+                x.zero_()
+            pa.pa_accept_drafts(out_tokens, accepted, target, draft, tokens, qs, uniforms, context_lens=ctx_in,
+                                context_lens_out=ctx_out, dev_status=status)
+            if wait:
+                torch.cuda.synchronize()
+            pa.pa_decode(out, q, kc, vc, tables, ctx_out, d**-0.5, ws, None)
+            torch.cuda.synchronize()
+            results.append((out.clone(), ctx_out.clone()))
+        assert int(status.item()) == pa.status_bit(-5)
+        assert all(torch.equal(x, y) for x, y in zip(*results)), i
+        lost = np.where(rows > 0, rows - 1, 0)
+        lost[-1] = 0
+        kept = np.where(np.arange(b) == b - 1, 0, accepted.cpu().numpy())
+        assert np.array_equal(results[0][1].cpu().numpy(), ctx - np.where(rows > 0, lost - kept, 0))
