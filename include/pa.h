@@ -438,8 +438,11 @@ PA_API void pa_calibration_clear(void);
  * more tokens than it has, or whose lengths contradict each other.  A refused
  * sequence's state stays as it was; its rows keep their place in query_start
  * and get position and slot -1.  A bad queue state or a bad block ID sets the
- * RANGE bit; the slot is -1 then.  Blocks shared between sequences are the host
- * allocator's: do not give them up here.  block_size 16 or 32;
+ * RANGE bit; the slot is -1 then.  A bad ID in a sequence that gives it up is
+ * reported by that step, and queued all the same (places in the queue are counted
+ * before the tables are read): take it out before a later step hands it on.
+ * Blocks shared between sequences are the host allocator's: do not give them up
+ * here.  block_size 16 or 32;
  * num_blocks * block_size and max_blocks_per_seq * block_size fit in int32.
  */
 PA_API int pa_step_slots(const int32_t* new_tokens, const int32_t* context_lens, int32_t* context_lens_out,

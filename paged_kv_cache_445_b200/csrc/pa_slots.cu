@@ -241,7 +241,9 @@ __global__ void __launch_bounds__(THREADS) slots_kernel(const SlotsParams p, int
           }
           long long at = head + place;
           if (at >= p.num_blocks) at -= p.num_blocks;
-          p.free_blocks[at] = row[sh.held[i] - back + k];
+          const int id = row[sh.held[i] - back + k];
+          if (id < 0 || id >= p.num_blocks) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));  // queued all the same
+          p.free_blocks[at] = id;
         }
       }
     }
