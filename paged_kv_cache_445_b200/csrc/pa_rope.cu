@@ -54,11 +54,15 @@ enum Pairs { PAIRS_NONE, PAIRS_HALF, PAIRS_INTERLEAVED };
 
 // Eight values a c + b s, each rounded once to bf16.  Two fused operations (the product's error added to the sum) leave
 // an error of at most 1.5 ulp of binary32, which decides the rounding only within 2 ulp of a tie; such a value, and an
-// infinity or NaN, is taken again in binary64, where both products are exact.  One vector in 1600 holds one.
+// infinity or NaN, is taken again in binary64, where both products are exact; their sum is not where one lies 2^-21
+// below the other, so it is rounded to odd from there on (the last bit kept tells that something follows): then one more
+// rounding is right.  One vector in 1600 holds one.
 __device__ __noinline__ float turn_exact(float a, float c, float b, float s) {
-  const double d = static_cast<double>(a) * c + static_cast<double>(b) * s;
-  const float z = __double2float_rz(d);  // round to odd: then one more rounding is right
-  return static_cast<double>(z) != d ? __uint_as_float(__float_as_uint(z) | 1) : z;
+  const double x = static_cast<double>(a) * c, y = static_cast<double>(b) * s;
+  const double d = __dadd_rz(x, y);
+  const float z = __double2float_rz(d);
+  const bool exact = static_cast<double>(z) == d && __dadd_rd(x, y) == __dadd_ru(x, y);
+  return exact ? z : __uint_as_float(__float_as_uint(z) | 1);
 }
 __device__ __forceinline__ uint4 turn(const float (&a)[8], const float (&b)[8], const float (&c)[8],
                                       const float (&s)[8]) {
