@@ -102,11 +102,14 @@ PA_API int pa_cache_append(const void* k_new, const void* v_new, void* k_cache, 
  * which decode calls do not use.
  *
  * Workspace contract: the caller allocates it and ZERO-FILLS it once before
- * its first use; it may then reuse it for any later call on the same stream.
- * The library keeps its counters in it and every call that returns PA_OK and
- * whose dev_status stays clear puts them back to zero; the rest is scratch.
- * Calls that overlap in time must use different workspaces.  After a call
- * that reported a device error, zero it again.
+ * its first use; it may then reuse it for any later call on the same stream with
+ * the same num_q_heads, num_kv_heads and head_dim, of up to num_query_tokens rows
+ * and max_blocks_per_seq * block_size keys a row, giving its whole size as
+ * workspace_bytes each time.  The library keeps its counters in it and every call
+ * that returns PA_OK and whose dev_status stays clear puts them back to zero; the
+ * rest is scratch.  Calls that overlap in time must use different workspaces.
+ * After a call that reported a device error, and before calls of other heads,
+ * zero it again.
  */
 PA_API size_t pa_workspace_bytes(int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim,
                                  int max_blocks_per_seq, int block_size);

@@ -200,7 +200,11 @@ int run_attention(void* out, const void* q, const int32_t* query_start, const vo
   const bool chunk_path = query_start && !kv_fp8 && chunk_supported(num_q_heads / num_kv_heads, head_dim);
   const size_t chunk_bytes =
       chunk_path ? chunk_part(total_q_tokens, num_q_heads, num_kv_heads, head_dim, di.num_sms) : 0;
-  if (workspace_bytes < rows_bytes + casc_bytes + chunk_bytes) return PA_ERR_WORKSPACE;
+  const size_t ws_end = workspace_bytes / 16 * 16;
+  if (ws_end < rows_bytes + casc_bytes + chunk_bytes) return PA_ERR_WORKSPACE;
+  // the scratch of the kernels beside the rows kernel's starts behind its own
+  const size_t segment_bytes = rows_segment_bytes(total_q_tokens, num_kv_heads);
+  void* const scratch = static_cast<uint8_t*>(workspace) + rows_bytes - segment_bytes;
   if (plan) {  // a plan made for this batch shape on a GPU of this size
     if (plan[PLAN_MAGIC] != PLAN_MAGIC_VALUE || plan[PLAN_NUM_SEQS] != num_seqs ||
         plan[PLAN_TOTAL_Q] != total_q_tokens || plan[PLAN_GROUP] != num_q_heads / num_kv_heads ||
@@ -241,7 +245,7 @@ int run_attention(void* out, const void* q, const int32_t* query_start, const vo
     p.k_inv_scale = 1.f / k_scale;
     p.v_inv_scale = 1.f / v_scale;
   }
-  rows_workspace_layout(workspace, total_q_tokens, num_q_heads, num_kv_heads, head_dim, max_keys, di.num_sms, &p);
+  rows_workspace_layout(workspace, ws_end, total_q_tokens, num_q_heads, num_kv_heads, head_dim, max_keys, di.num_sms, &p);
   p.num_sms = di.num_sms;
   p.weighted = di.num_sms <= PA_MAX_WEIGHTED_SMS && sm_rates_snapshot(p.sm_rate, di.num_sms) ? 1 : 0;
   if (ovr) {
@@ -264,7 +268,7 @@ int run_attention(void* out, const void* q, const int32_t* query_start, const vo
   p.group_start = group_start;
   p.group_prefix = group_prefix;
   p.num_groups = num_groups;
-  p.casc_partials = num_groups > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + rows_bytes) : nullptr;
+  p.casc_partials = num_groups > 0 ? static_cast<float*>(scratch) : nullptr;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (num_groups > 0) {
     // the shared prefixes first: per-slice partials that the rows kernel folds in
@@ -335,8 +339,8 @@ int run_attention(void* out, const void* q, const int32_t* query_start, const vo
     c.num_blocks = num_blocks;
     c.scale_log2 = p.scale_log2;
     c.status = dev_status;
-    chunk_workspace_layout(static_cast<uint8_t*>(workspace) + rows_bytes, total_q_tokens,
-                           multirow_seq_bound(total_q_tokens), num_kv_heads, p.group, di.num_sms, &c);
+    chunk_workspace_layout(scratch, static_cast<uint8_t*>(workspace) + ws_end - segment_bytes, total_q_tokens,
+                           multirow_seq_bound(total_q_tokens), num_kv_heads, p.group, &c);
     p.skip_multi = 1;
     if (run_chunk && run_rows && decode_ctas > 0 && decode_ctas < di.num_sms) {
       // the decode rows first, on decode_ctas SMs; they release the chunk

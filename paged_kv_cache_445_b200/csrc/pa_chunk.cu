@@ -862,13 +862,12 @@ size_t chunk_workspace_bytes(int num_query_tokens, int num_seqs_bound, int num_k
   return round256_c(counters) + slots;
 }
 
-void chunk_workspace_layout(void* ws, int num_query_tokens, int num_seqs_bound, int num_kv_heads, int group,
-                            int num_sms, ChunkParams* p) {
-  (void)num_sms;
-  uint8_t* b = static_cast<uint8_t*>(ws);
-  p->counters = reinterpret_cast<int*>(b);
-  b += round256_c(chunk_max_items(num_query_tokens, num_seqs_bound, num_kv_heads, group) * 2 * CH_M * sizeof(int));
-  p->partials = reinterpret_cast<float*>(b);
+void chunk_workspace_layout(void* scratch, void* counters_end, int num_query_tokens, int num_seqs_bound,
+                            int num_kv_heads, int group, ChunkParams* p) {
+  p->partials = static_cast<float*>(scratch);
+  p->counters = reinterpret_cast<int*>(
+      static_cast<uint8_t*>(counters_end) -
+      round256_c(chunk_max_items(num_query_tokens, num_seqs_bound, num_kv_heads, group) * 2 * CH_M * sizeof(int)));
 }
 
 int launch_chunk(const ChunkParams& p, const void* q, const void* k_cache, const void* v_cache, int total_q_tokens,

@@ -231,10 +231,11 @@ struct ChunkParams {
 };
 
 // Workspace of the chunk kernel's pieces for a batch of at most
-// num_query_tokens rows, and its carving (after the rows kernel's part).
+// num_query_tokens rows, and its carving: the pieces from `scratch` on (after the
+// rows kernel's scratch), the counters up to `counters_end` (before its segments).
 size_t chunk_workspace_bytes(int num_query_tokens, int num_seqs_bound, int num_kv_heads, int group, int num_sms);
-void chunk_workspace_layout(void* ws, int num_query_tokens, int num_seqs_bound, int num_kv_heads, int group,
-                            int num_sms, ChunkParams* p);
+void chunk_workspace_layout(void* scratch, void* counters_end, int num_query_tokens, int num_seqs_bound,
+                            int num_kv_heads, int group, ChunkParams* p);
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -267,11 +268,17 @@ int launch_append_fp8(const void* k_new, const void* v_new, void* k_cache, void*
 int launch_rows(const RowsParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv, int head_dim,
                 cudaStream_t stream, int num_sms, int ctas = 0);
 // Workspace of the rows kernel for at most num_rows query rows on a device with
-// num_sms SMs, and the carving of a buffer of that size into RowsParams.
-// max_keys bounds the keys of any row (max_blocks_per_seq * block_size).
+// num_sms SMs, and the carving of a buffer of that size or larger into
+// RowsParams.  max_keys bounds the keys of any row (max_blocks_per_seq *
+// block_size).  What has to read zero when a call starts lies at the front where
+// its size is fixed, and at the end (ws_end, in bytes, a multiple of 16) where it
+// grows with the call; the scratch that a call leaves behind grows from the front
+// and the two never meet, whatever sizes the calls before had, up to those the
+// buffer was made for.
 size_t rows_workspace_bytes(int num_rows, int num_q_heads, int num_kv_heads, int head_dim, long long max_keys,
                             int num_sms);
-void rows_workspace_layout(void* ws, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
+size_t rows_segment_bytes(int num_rows, int num_kv_heads);  // of that, the part at the end
+void rows_workspace_layout(void* ws, size_t ws_end, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
                            long long max_keys, int num_sms, RowsParams* p);
 int rows_supported(int group, int head_dim);
 int chunk_supported(int group, int head_dim);

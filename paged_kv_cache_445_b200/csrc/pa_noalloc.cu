@@ -129,17 +129,19 @@ extern "C" int pa_decode_static_scratch(void* out, const void* q, const void* k_
   void* ws = nullptr;
   int rc = pa::scratch_for_current_device(&ws);
   if (rc != PA_OK) return rc;
-  // the leading part of the workspace (counters, then segment records, up to
-  // the piece table) must read zero when the kernel starts
+  // what must read zero when the kernel starts lies at the front (the counters, up to the piece table) and at the end
+  // (the segment records): both in one call, as two rows as wide as the longer one
   pa::RowsParams lay{};
   pa::DeviceInfo di;
   if ((rc = pa::device_info(&di)) != PA_OK) return rc;
-  pa::rows_workspace_layout(ws, num_seqs, num_q_heads, num_kv_heads, head_dim,
+  pa::rows_workspace_layout(ws, PA_STATIC_SCRATCH_BYTES, num_seqs, num_q_heads, num_kv_heads, head_dim,
                             static_cast<long long>(max_blocks_per_seq) * block_size, di.num_sms, &lay);
-  const size_t zero_bytes =
-      static_cast<size_t>(reinterpret_cast<unsigned char*>(lay.table) - static_cast<unsigned char*>(ws));
-  const cudaError_t e = cudaMemsetAsync(ws, 0, zero_bytes, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return pa::cuda_fail(e, "cudaMemsetAsync");
+  const size_t front = static_cast<size_t>(reinterpret_cast<unsigned char*>(lay.table) - static_cast<unsigned char*>(ws));
+  const size_t back = pa::rows_segment_bytes(num_seqs, num_kv_heads);
+  const size_t width = front > back ? front : back;
+  const cudaError_t e = cudaMemset2DAsync(ws, PA_STATIC_SCRATCH_BYTES - width, 0, width, 2,
+                                          static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return pa::cuda_fail(e, "cudaMemset2DAsync");
   return pa::run_attention(out, q, nullptr, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
                            num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
                            ws, PA_STATIC_SCRATCH_BYTES, dev_status, stream);

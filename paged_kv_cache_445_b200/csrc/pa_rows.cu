@@ -1419,27 +1419,29 @@ static size_t partials_bytes(int num_q_heads, int num_kv_heads, int head_dim, in
 
 static size_t verify_counter_bytes(int num_sms) { return round256(static_cast<size_t>(num_sms) * sizeof(int)); }
 
+size_t rows_segment_bytes(int num_rows, int num_kv_heads) {
+  return round256(static_cast<size_t>(num_rows) * num_kv_heads * sizeof(long long));
+}
+
 size_t rows_workspace_bytes(int num_rows, int num_q_heads, int num_kv_heads, int head_dim, long long max_keys,
                             int num_sms) {
   return SCHED_BYTES + verify_counter_bytes(num_sms) +
-         round256(static_cast<size_t>(num_rows) * num_kv_heads * sizeof(long long)) +
          round256(table_entries(num_rows, num_kv_heads, max_keys) * sizeof(long long)) +
-         partials_bytes(num_q_heads, num_kv_heads, head_dim, num_sms);
+         partials_bytes(num_q_heads, num_kv_heads, head_dim, num_sms) + rows_segment_bytes(num_rows, num_kv_heads);
 }
 
-void rows_workspace_layout(void* ws, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
+void rows_workspace_layout(void* ws, size_t ws_end, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
                            long long max_keys, int num_sms, RowsParams* p) {
   (void)num_q_heads;
   (void)head_dim;
   uint8_t* b = static_cast<uint8_t*>(ws);
+  p->seginfo = reinterpret_cast<long long*>(b + ws_end - rows_segment_bytes(num_rows, num_kv_heads));
   p->sched = reinterpret_cast<int*>(b);
   p->sm_mask = reinterpret_cast<unsigned*>(b) + 8;
   p->sm_slots = reinterpret_cast<int*>(b) + 16;
   b += SCHED_BYTES;
   p->verify_counters = reinterpret_cast<int*>(b);
   b += verify_counter_bytes(num_sms);
-  p->seginfo = reinterpret_cast<long long*>(b);
-  b += round256(static_cast<size_t>(num_rows) * num_kv_heads * sizeof(long long));
   p->table = reinterpret_cast<long long*>(b);
   p->table_len = static_cast<long long>(table_entries(num_rows, num_kv_heads, max_keys));
   b += round256(table_entries(num_rows, num_kv_heads, max_keys) * sizeof(long long));
