@@ -566,7 +566,9 @@ PA_API int pa_cache_read_int4(float* k_out, float* v_out, const void* k_cache, c
  *
  * pa_int4_workspace_bytes: bytes of workspace on the CURRENT device, for any
  * batch of these heads; contract of pa_workspace_bytes (zero-filled once, one
- * workspace per call in flight).  Returns 0 for invalid sizes.
+ * workspace per call in flight).  A workspace of pa_workspace_bytes for these
+ * heads is large enough as well, and may serve calls on caches of either kind in
+ * turn.  Returns 0 for invalid sizes.
  */
 PA_API size_t pa_int4_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim);
 PA_API int pa_decode_int4(void* out, const void* q, const void* k_cache, const void* v_cache,

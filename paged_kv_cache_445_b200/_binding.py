@@ -673,7 +673,8 @@ def pa_int4_workspace_bytes(num_q_heads: int, num_kv_heads: int, head_dim: int) 
 
 
 def make_int4_workspace(num_q_heads: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
-    """A zero-filled workspace for pa_decode_int4 / pa_prefill_chunk_int4 (the zero fill is required once)."""
+    """A zero-filled workspace for pa_decode_int4 / pa_prefill_chunk_int4 (the zero fill is required once; one from
+    make_workspace for the same heads does too, and serves calls on other caches in turn)."""
     with torch.cuda.device(device):  # None: the current device
         n = pa_int4_workspace_bytes(num_q_heads, num_kv_heads, head_dim)
         return torch.zeros(n, dtype=torch.uint8, device="cuda")

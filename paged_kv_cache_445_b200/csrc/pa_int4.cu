@@ -67,8 +67,8 @@ namespace pa {
 namespace {
 
 constexpr int I4_FEW = 6;             // pieces of an item across CTAs that one warp merges
-constexpr int I4_WARP_COUNTERS = 512; // counters: per CTA, then (from here) per warp
-constexpr size_t I4_COUNTER_BYTES = 4 * (512 + 512 * 16);
+constexpr int I4_MAX_CTAS = 256;      // the counters, one word per CTA, then four bits for each of its warps, fill the
+                                      // 2048 bytes that the other attention kernels keep at zero between calls too
 constexpr int I4_FOLD = 8;             // units between two corrections of O
 constexpr float I4_NO_MAX = -3e38f; // maximum over no pieces
 constexpr float I4_TOP = 13.f;        // a weight's largest power of two; beside it a scale may be below 4
@@ -108,7 +108,7 @@ struct Int4Params {
   int num_seqs, num_rows, max_blocks, num_q_heads, num_kv_heads, group, rows_per_item, block_shift, num_blocks;
   float scale_log2;
   int* status;
-  int* counters;        // workspace: pieces brought per CTA or warp that an item starts in; zero between calls
+  unsigned* counters;   // workspace: pieces brought per CTA or warp that an item starts in; zero between calls
   float* warp_pieces;   // workspace: [CTA][warp][2]
   float* cta_pieces;    // workspace: [CTA][2]
 };
@@ -988,8 +988,11 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
             __threadfence();
             __syncwarp();
             if (lane == 0) {
-              got = atomicAdd(p.counters + I4_WARP_COUNTERS + w0, 1);
-              if (got == n - 1) p.counters[I4_WARP_COUNTERS + w0] = 0;
+              static_assert(WARPS == 8 && I4_FEW < 16, "four bits a warp");
+              unsigned* const word = p.counters + I4_MAX_CTAS + w0 / WARPS;
+              const int at = w0 % WARPS * 4;
+              got = atomicAdd(word, 1u << at) >> at & 15;
+              if (got == n - 1) atomicSub(word, static_cast<unsigned>(n) << at);
             }
             got = __shfl_sync(FULL_MASK, got, 0);
             __threadfence();
@@ -1132,7 +1135,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
     const int f = tid ? from[1] : from[0], n = tid ? count[1] : count[0];
     bool last = false;
     if (n > 0) {
-      last = atomicAdd(p.counters + f, 1) == n - 1;
+      last = atomicAdd(p.counters + f, 1u) == static_cast<unsigned>(n - 1);
       if (last) p.counters[f] = 0;
     }
     sh_merge[tid] = last;
@@ -1153,7 +1156,7 @@ __global__ void __launch_bounds__(I4<D, NT>::THREADS, 1) int4_kernel(const __gri
 template <int D, int NT>
 size_t workspace_of(int num_sms) {
   using C = I4<D, NT>;
-  return I4_COUNTER_BYTES + sizeof(float) * static_cast<size_t>(num_sms) * 2 * C::PIECE * (C::WARPS + 1);
+  return attention_counter_bytes(num_sms) + sizeof(float) * static_cast<size_t>(num_sms) * 2 * C::PIECE * (C::WARPS + 1);
 }
 
 size_t int4_workspace(int head_dim, int num_sms) {
@@ -1172,8 +1175,10 @@ int launch_int4(Int4Params& p, void* workspace, cudaStream_t stream, int num_sms
   // An item's start and end cost about a unit: counted where items are many (80.8 -> 79.6 us on 128 sequences), not
   // where a unit more would only cut short items in two.
   p.pad = 4ll * p.num_seqs * p.num_kv_heads >= static_cast<long long>(num_sms) * C::WARPS ? 1 : 0;
-  p.counters = static_cast<int*>(workspace);
-  p.warp_pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + I4_COUNTER_BYTES);
+  p.counters = static_cast<unsigned*>(workspace);
+  // The pieces take what the bf16 and FP8 kernels use for theirs (fewer bytes than those on every shape), so that one
+  // workspace may serve all three caches.
+  p.warp_pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attention_counter_bytes(num_sms));
   p.cta_pieces = p.warp_pieces + static_cast<size_t>(num_sms) * 2 * C::PIECE * C::WARPS;
   static PerDevice ready;
   int done = 0;
@@ -1217,7 +1222,7 @@ int run_int4(void* out, const void* q, const int32_t* query_start, const void* k
   DeviceInfo di;
   const int rc = device_info(&di);
   if (rc != PA_OK) return rc;
-  if (di.num_sms > I4_WARP_COUNTERS) return PA_ERR_UNSUPPORTED;
+  if (di.num_sms > I4_MAX_CTAS) return PA_ERR_UNSUPPORTED;
   if (workspace_bytes < int4_workspace(head_dim, di.num_sms)) return PA_ERR_WORKSPACE;
   Int4Params p{};
   p.out = static_cast<__nv_bfloat16*>(out);

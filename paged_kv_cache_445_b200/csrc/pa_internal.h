@@ -277,7 +277,8 @@ int launch_rows(const RowsParams& p, const CUtensorMap& tmk, const CUtensorMap& 
 // buffer was made for.
 size_t rows_workspace_bytes(int num_rows, int num_q_heads, int num_kv_heads, int head_dim, long long max_keys,
                             int num_sms);
-size_t rows_segment_bytes(int num_rows, int num_kv_heads);  // of that, the part at the end
+size_t attention_counter_bytes(int num_sms);                // of that, the counters at the front
+size_t rows_segment_bytes(int num_rows, int num_kv_heads);  // and the part at the end
 void rows_workspace_layout(void* ws, size_t ws_end, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
                            long long max_keys, int num_sms, RowsParams* p);
 int rows_supported(int group, int head_dim);

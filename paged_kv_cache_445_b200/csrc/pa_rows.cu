@@ -1419,13 +1419,15 @@ static size_t partials_bytes(int num_q_heads, int num_kv_heads, int head_dim, in
 
 static size_t verify_counter_bytes(int num_sms) { return round256(static_cast<size_t>(num_sms) * sizeof(int)); }
 
+size_t attention_counter_bytes(int num_sms) { return SCHED_BYTES + verify_counter_bytes(num_sms); }
+
 size_t rows_segment_bytes(int num_rows, int num_kv_heads) {
   return round256(static_cast<size_t>(num_rows) * num_kv_heads * sizeof(long long));
 }
 
 size_t rows_workspace_bytes(int num_rows, int num_q_heads, int num_kv_heads, int head_dim, long long max_keys,
                             int num_sms) {
-  return SCHED_BYTES + verify_counter_bytes(num_sms) +
+  return attention_counter_bytes(num_sms) +
          round256(table_entries(num_rows, num_kv_heads, max_keys) * sizeof(long long)) +
          partials_bytes(num_q_heads, num_kv_heads, head_dim, num_sms) + rows_segment_bytes(num_rows, num_kv_heads);
 }
