@@ -562,7 +562,8 @@ PA_API int pa_cache_read_int4(float* k_out, float* v_out, const void* k_cache, c
  * up to rounding.  The append is a call of its own (pa_rope_append_int4,
  * pa_cache_append_int4).  Rows of q behind query_start[num_seqs] are not read
  * and their output is left as it was.  Keys in a bad block are skipped, with the
- * RANGE bit.
+ * RANGE bit.  A negative length counts as none: the sequence's rows are zeros,
+ * and no status is set.  One longer than its table gives zeros and the RANGE bit.
  *
  * pa_int4_workspace_bytes: bytes of workspace on the CURRENT device, for any
  * batch of these heads; contract of pa_workspace_bytes (zero-filled once, one
