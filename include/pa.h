@@ -405,7 +405,9 @@ PA_API void pa_calibration_clear(void);
  * The step around the attention: tables and slots from request lengths, rotary
  * positions with the append, a cache held in 4 bits, verification of drafts.
  * With these calls a step runs from lengths to accepted tokens without the
- * host, and can be captured in a CUDA graph.
+ * host, and can be captured in a CUDA graph.  They take up to 2^31 - 65537
+ * sequences (pa_accept_drafts: 2^28 - 1) and values in a row of probabilities,
+ * and answer PA_ERR_SHAPE past that.
  * ---------------------------------------------------------------------------
  *
  * pa_step_slots -- block tables, row offsets, positions and slots of a step,

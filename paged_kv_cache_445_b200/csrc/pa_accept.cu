@@ -340,7 +340,7 @@ extern "C" int pa_accept_drafts(int32_t* out_tokens, int32_t* num_accepted, cons
                                 void* stream) {
   if (num_seqs < 0 || total_rows < 0 || vocab <= 0 || target_stride < vocab) return PA_ERR_SHAPE;
   if (draft_probs && draft_stride < vocab) return PA_ERR_SHAPE;
-  if (num_seqs > INT32_MAX / 8) return PA_ERR_SHAPE;
+  if (num_seqs > INT32_MAX / 8 || vocab > pa::PA_MAX_COUNT) return PA_ERR_SHAPE;
   if ((context_lens == nullptr) != (context_lens_out == nullptr)) return PA_ERR_NULL;
   if (num_seqs == 0) return PA_OK;
   if (!num_accepted || !query_start) return PA_ERR_NULL;

@@ -1211,6 +1211,7 @@ int run_int4(void* out, const void* q, const int32_t* query_start, const void* k
   if (num_seqs < 0 || total_rows < 0 || max_blocks <= 0 || num_blocks <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
       num_q_heads % num_kv_heads)
     return PA_ERR_SHAPE;
+  if (num_seqs > PA_MAX_COUNT) return PA_ERR_SHAPE;
   const int group = num_q_heads / num_kv_heads;
   if (block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
   if (!rows_supported(group, head_dim)) return PA_ERR_UNSUPPORTED;

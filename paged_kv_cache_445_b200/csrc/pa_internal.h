@@ -67,6 +67,10 @@ void sm_rates_clear();
 // tile counts in shared memory (larger batches scan context_lens instead).
 constexpr int ROWS_SMEM_SEQS_HOST = 1024;
 
+// Sequences, and values of a probability row, that the step operators take: their loops run past the end by less than
+// this, in 32 bits.
+constexpr int PA_MAX_COUNT = INT32_MAX - 65536;
+
 // Parameters of the single-row attention kernel (decode rows, and the rows of
 // any sequence the chunk kernel does not take).
 struct RowsParams {

@@ -306,6 +306,7 @@ extern "C" int pa_step_slots(const int32_t* new_tokens, const int32_t* context_l
                              int32_t* query_start, int32_t* positions, int32_t* slot_mapping, int max_tokens,
                              int* dev_status, void* stream) {
   if (num_seqs < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_tokens < 0) return PA_ERR_SHAPE;
+  if (num_seqs > pa::PA_MAX_COUNT) return PA_ERR_SHAPE;
   if (block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_blocks) * block_size > INT32_MAX) return PA_ERR_SHAPE;  // slots are int32
   if (static_cast<long long>(max_blocks_per_seq) * block_size > INT32_MAX) return PA_ERR_SHAPE;
