@@ -116,13 +116,20 @@ __global__ void __launch_bounds__(ACC_THREADS, 2) accept_kernel(const AcceptPara
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int start = p.query_start[s], end = p.query_start[s + 1];
   const int rows = end - start;
-  const bool bad = start < 0 || end < start || end > p.total_rows;
-  if (bad || rows == 0) {  // uniform over the cluster: all its CTAs leave
+  if (start < 0 || end < start || end > p.total_rows) {  // uniform over the cluster: all its CTAs leave
     if (rank == 0 && tid == 0) {
-      if (bad) set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
+      set_status(p.status, PA_STATUS_BIT(PA_ERR_RANGE));
       p.num_accepted[s] = 0;
       if (p.context_lens) p.context_lens_out[s] = p.context_lens[s];
       __threadfence();  // an attention kernel launched behind this one reads the lengths in its prologue
+    }
+    return;
+  }
+  if (rows == 0) {
+    if (rank == 0 && tid == 0) {
+      p.num_accepted[s] = 0;
+      if (p.context_lens) p.context_lens_out[s] = p.context_lens[s];
+      __threadfence();  // (as above)
     }
     return;
   }
