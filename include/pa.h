@@ -561,11 +561,14 @@ PA_API int pa_cache_read_int4(float* k_out, float* v_out, const void* k_cache, c
 /*
  * pa_decode_int4 / pa_prefill_chunk_int4 -- pa_decode and pa_prefill_chunk over
  * a 4-bit cache: the same arguments, shapes (head_dim 64, 128, 256) and results
- * up to rounding.  The append is a call of its own (pa_rope_append_int4,
- * pa_cache_append_int4).  Rows of q behind query_start[num_seqs] are not read
- * and their output is left as it was.  Keys in a bad block are skipped, with the
- * RANGE bit.  A negative length counts as none: the sequence's rows are zeros,
- * and no status is set.  One longer than its table gives zeros and the RANGE bit.
+ * up to rounding.  Rows of a sequence are taken 16 / group at a time (8 / group at
+ * head_dim 256), one pass over the keys each: made for verification rows and
+ * short chunks; a long prompt is faster on the bf16 cache.  The append is a call of
+ * its own (pa_rope_append_int4, pa_cache_append_int4).  Rows of q behind
+ * query_start[num_seqs] are not read and their output is left as it was.  Keys in
+ * a bad block are skipped, with the RANGE bit.  A negative length counts as none:
+ * the sequence's rows are zeros, and no status is set.  One longer than its table
+ * gives zeros and the RANGE bit.
  *
  * pa_int4_workspace_bytes: bytes of workspace on the CURRENT device, for any
  * batch of these heads; contract of pa_workspace_bytes (zero-filled once, one
