@@ -46,9 +46,10 @@
 //    neither leaves fp16's range, a chunk's scales enter times a power of two that
 //    puts the largest one the warp met in the item between 1/2 and 1: it moves when
 //    a unit holds one past 2 (the vote that m needs tells it), O with it.  A unit's
-//    scales are multiplied in place, by one lane each.  Products down to 2^-26 of
-//    the largest keep all of fp16's bits, less ones lose them gradually and are
-//    nothing at 2^-37.  (Scales taken as they are: 74 us in place of 78 on the batch
+//    scales are multiplied in place, by one lane each.  Scales down to 2^-13 of the
+//    chunk's largest and products down to 2^-26 of the largest keep all of fp16's
+//    bits; less ones lose them gradually, a scale at 2^-24 or a product at 2^-37
+//    the last.  (Scales taken as they are: 74 us in place of 78 on the batch
 //    above, and outputs past their bound where |V| is below 1e-3.)
 //  - the 8 too many are one product of constants with P s per chunk, taken off O
 //    every 8 units, before they outgrow what O's last bits can tell.
